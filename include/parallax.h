@@ -82,6 +82,7 @@ extern "C" {
 #define PARALLAX_ERR_DEVICE_TIMEOUT (-9)
 #define PARALLAX_ERR_BAD_PHASE (-10)
 #define PARALLAX_ERR_SEQLEN_CLAMPED (-11)
+#define PARALLAX_ERR_POSITION_CLAMPED (-13)
 
 #define PARALLAX_DTYPE_BF16 0
 #define PARALLAX_DTYPE_F32 1
@@ -95,6 +96,7 @@ extern "C" {
 /* Bits of the device status word kept at the start of the workspace. */
 #define PARALLAX_DEVICE_STATUS_TIMEOUT 1u
 #define PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED 2u
+#define PARALLAX_DEVICE_STATUS_POSITION_CLAMPED 4u
 
 /*
  * Number of key-range partitions (CTAs of the persistent split-KV kernel) the
@@ -345,12 +347,171 @@ int parallax_varlen_prefill(const void* q, const void* r, const void* k, const v
                             size_t workspace_bytes);
 
 /*
+ * Norm and rotation of the query, probe and key heads
+ * ---------------------------------------------------
+ * What a layer does between its projections and the attention above, in one
+ * pass over the rows: each head row x of D values gets an RMS norm over its
+ * own D values with a learned weight, and its first rotary_dim dimensions are
+ * rotated by the token's position:
+ *     n = x / sqrt(mean(x^2) + eps) * weight        (weight NULL: n = x)
+ *     y_a = n_a cos_p - n_b sin_p,  y_b = n_a sin_p + n_b cos_p
+ * for pair p of dimensions (a, b) = (p, p + rotary_dim / 2), or (2p, 2p + 1)
+ * with interleaved != 0; dimensions from rotary_dim on are not rotated. All
+ * arithmetic is fp32, rounded once to dtype. The pages' models are Qwen-3
+ * ones ("Integrazioni AI personalizzate dopo l'attenzione Parallax"), whose
+ * layers norm and rotate the heads this way; the probe is query-like (same
+ * page, W_R acting on the layer input), so it may be normed and rotated too.
+ *
+ * Shared by the three entry points:
+ *  - q [tokens][Hq][D] and k [tokens][Hkv][D]; r like q, or NULL: no probe
+ *    (r_out, r_weight and their gradients are then not used). Heads are D
+ *    elements apart and tokens q_stride, r_stride, k_stride elements (at least
+ *    heads * D, a multiple of 16 bytes), so that slices of a fused projection
+ *    are taken as they are.
+ *  - dtype: PARALLAX_DTYPE_BF16 or PARALLAX_DTYPE_F32, of the rows, the
+ *    weights [D] and the outputs.
+ *  - cos_sin [max_positions][rotary_dim] fp32: a position's rotary_dim / 2
+ *    cosines, then its sines (parallax_rope_table writes the plain kind).
+ *    rotary_dim is a multiple of 16, 16 .. D.
+ *  - positions [tokens] int32. A position outside [0, max_positions) is
+ *    clamped into it and sets PARALLAX_DEVICE_STATUS_POSITION_CLAMPED.
+ *  - eps > 0, finite. Row, weight and table pointers 16-byte aligned.
+ *  - workspace: its first 256 bytes (zeroed once) hold the device status word.
+ * Errors as parallax_decode (PARALLAX_ERR_BAD_SHAPE for strides, eps,
+ * rotary_dim and the like).
+ */
+
+/*
+ * cos_sin[t][p] = cos(t base^(-2p / rotary_dim)) and cos_sin[t][rotary_dim / 2
+ * + p] = the sine, the angle in fp64. rotary_dim a multiple of 16, 16 .. 128;
+ * base positive and finite; cos_sin 16-byte aligned.
+ */
+int parallax_rope_table(float* cos_sin, int max_positions, int rotary_dim, double base,
+                        void* stream);
+
+/*
+ * The forward pass.
+ *  - positions NULL: token t is at position t (t % seq_len with seq_len > 0).
+ *  - seq_len = 0: the outputs are [tokens][H][D], the packed layout of
+ *    parallax_varlen_prefill (and of the decode, for one token per sequence).
+ *    seq_len = L > 0 (tokens a multiple of L): they are [tokens / L][H][L][D],
+ *    the layout of parallax_prefill.
+ *  - q_out may be q (r_out r, k_out k) when seq_len = 0 and the rows are
+ *    contiguous; otherwise outputs and inputs must not overlap.
+ */
+int parallax_qk_norm_rope(const void* q, const void* r, const void* k, const void* q_weight,
+                          const void* r_weight, const void* k_weight, const float* cos_sin,
+                          const int32_t* positions, void* q_out, void* r_out, void* k_out,
+                          int tokens, int Hq, int Hkv, int D, int rotary_dim, int interleaved,
+                          int max_positions, float eps, long long q_stride, long long r_stride,
+                          long long k_stride, int seq_len, int dtype, void* stream,
+                          void* workspace, size_t workspace_bytes);
+
+/*
+ * The backward pass of parallax_qk_norm_rope: from the gradients dq_out,
+ * dr_out, dk_out of its outputs (in their layout, contiguous) and its inputs,
+ * the gradients dq, dr, dk of the rows (tokens dq_stride, ... elements apart,
+ * so that they may be slices of one buffer) and, for each weight given, its
+ * gradient [D] in fp32, summed over all tokens and heads. With
+ *   xh = x / sqrt(mean(x^2) + eps),  dz = dy rotated back,  dn = dz weight:
+ *   dx = (dn - xh mean(dn xh)) / sqrt(mean(x^2) + eps),  dweight = sum dz xh.
+ *  - dq may be dq_out (and so on) when seq_len = 0 and dq_stride = Hq * D; no
+ *    other overlap. q (r, k) is not read where its weight is NULL.
+ *  - Results are bitwise reproducible (no atomics).
+ *  - workspace: parallax_qk_norm_rope_backward_workspace_bytes; concurrent
+ *    calls need separate workspaces.
+ */
+int parallax_qk_norm_rope_backward(
+    const void* dq_out, const void* dr_out, const void* dk_out, const void* q, const void* r,
+    const void* k, const void* q_weight, const void* r_weight, const void* k_weight,
+    const float* cos_sin, const int32_t* positions, void* dq, void* dr, void* dk,
+    float* dq_weight, float* dr_weight, float* dk_weight, int tokens, int Hq, int Hkv, int D,
+    int rotary_dim, int interleaved, int max_positions, float eps, long long q_stride,
+    long long r_stride, long long k_stride, long long dq_stride, long long dr_stride,
+    long long dk_stride, int seq_len, int dtype, void* stream, void* workspace,
+    size_t workspace_bytes);
+
+/* Workspace bytes of parallax_qk_norm_rope_backward on the current device: the
+ * status header and one [D] fp32 partial sum per block. 0 for bad arguments. */
+size_t parallax_qk_norm_rope_backward_workspace_bytes(int tokens, int Hq, int Hkv, int D);
+
+/*
+ * The forward pass for new tokens of sequences with a paged cache: q and r are
+ * written out, k goes (normed and rotated) and v (as it is) into the pools of
+ * parallax_decode_paged, in the same pass.
+ *  - v [total_tokens][Hkv][D], tokens v_stride elements apart; q_out, r_out
+ *    [total_tokens][Hq][D]; k_pages, v_pages, block_table and page_size as
+ *    parallax_decode_paged (dtype for all; any page_size >= 1).
+ *  - cu_seqlens_q [B + 1] int32, non-decreasing: sequence b's new tokens are
+ *    rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1. NULL: one token per sequence
+ *    (total_tokens = B). Rows outside cu_seqlens_q[0] .. cu_seqlens_q[B]-1 (a
+ *    padded batch) are neither read nor written.
+ *  - cache_seqlens [B] int32: the sequences' lengths AFTER the append, as the
+ *    attention call that follows takes them. With c new tokens, token j of a
+ *    sequence becomes key cache_seqlens[b] - c + j. A key outside the block
+ *    table or in a page outside the pool is not written and sets
+ *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED. Two tokens with one slot (a page
+ *    listed for two sequences): one of them is kept.
+ *  - positions NULL: a token's position is its key index.
+ */
+int parallax_norm_rope_append(
+    const void* q, const void* r, const void* k, const void* v, const void* q_weight,
+    const void* r_weight, const void* k_weight, const float* cos_sin, const int32_t* positions,
+    const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, const int32_t* block_table,
+    void* q_out, void* r_out, void* k_pages, void* v_pages, int B, int total_tokens, int Hq,
+    int Hkv, int D, int rotary_dim, int interleaved, int max_positions, float eps,
+    long long q_stride, long long r_stride, long long k_stride, long long v_stride, int num_pages,
+    int page_size, int max_pages_per_seq, int dtype, void* stream, void* workspace,
+    size_t workspace_bytes);
+
+/*
+ * Attention of a chunk of new tokens over a paged cache that already holds
+ * them (chunked prefill, a mixed batch of chunks and single tokens, or drafted
+ * tokens to be checked): parallax_varlen_prefill's rows over
+ * parallax_decode_paged's keys.
+ *  - q, r, out [total_tokens][Hq][D] bf16; k_pages, v_pages, block_table,
+ *    num_pages, page_size and max_pages_per_seq as parallax_decode_paged, the
+ *    pools bf16.
+ *  - cu_seqlens_q [B + 1] int32, non-decreasing: sequence b's rows. Any number
+ *    per sequence, 0 included. Rows outside cu_seqlens_q[0] ..
+ *    cu_seqlens_q[B]-1 are left as they are. NULL: one token per sequence
+ *    (total_tokens = B); the call is then parallax_decode_paged.
+ *  - cache_seqlens [B] int32: keys held, the new tokens' included. With c new
+ *    tokens, row j of sequence b attends keys 0 .. cache_seqlens[b] - c + j
+ *    (causal != 0) or all cache_seqlens[b]; a row that sees no key is 0.
+ *    Lengths and bounds outside their ranges are clamped and set
+ *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED, as does a causal sequence with
+ *    more new tokens than keys.
+ *  - Slots past a sequence's length may hold anything. Keys and values below
+ *    it must be finite: a row's tiles include keys behind the row's position.
+ *  - A page id outside [0, num_pages) is not read: its keys are left out and
+ *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED is set.
+ *  - probe != 0: the Parallax output (r required); probe == 0: softmax.
+ *  - Hq / Hkv at most 128; scale positive and finite.
+ *  - workspace: parallax_prefill_paged_workspace_bytes, the first 256 bytes
+ *    zeroed once; the rest (partial records) is rewritten by every call, so
+ *    concurrent calls need separate workspaces.
+ * Errors as parallax_decode. Results are bitwise reproducible on one device.
+ */
+int parallax_prefill_paged(const void* q, const void* r, const void* k_pages, const void* v_pages,
+                           const int32_t* block_table, const int32_t* cu_seqlens_q,
+                           const int32_t* cache_seqlens, void* out, int B, int total_tokens,
+                           int Hq, int Hkv, int D, float scale, int causal, void* stream,
+                           int num_pages, int page_size, int max_pages_per_seq, int probe,
+                           void* workspace, size_t workspace_bytes);
+
+/* Workspace bytes of parallax_prefill_paged on the current device, whatever
+ * the lengths. 0 for bad arguments. */
+size_t parallax_prefill_paged_workspace_bytes(int B, int total_tokens, int Hq, int Hkv, int D);
+
+/*
  * Synchronise the current device, then read (and, if clear != 0, zero) the
  * device status word at the start of a workspace. *device_status receives PARALLAX_DEVICE_STATUS_* bits;
  * the return value maps them to a status: PARALLAX_ERR_DEVICE_TIMEOUT if a
  * bounded wait inside a kernel gave up (the kernel then returned early and its
  * output is invalid), PARALLAX_ERR_SEQLEN_CLAMPED if a length was outside
- * [0, Lmax], else PARALLAX_OK.
+ * [0, Lmax], PARALLAX_ERR_POSITION_CLAMPED if a rotary position was outside
+ * its table, else PARALLAX_OK.
  */
 int parallax_workspace_status(void* workspace, int clear, uint32_t* device_status);
 

@@ -43,6 +43,18 @@ int parallax_testing_prefill_stalled(const void* q, const void* r, const void* k
                                      float scale, int causal, void* stream, int out_dtype,
                                      void* workspace, size_t workspace_bytes, int timeout_ms);
 
+/*
+ * parallax_prefill_paged (cu_seqlens_q required) with the same two changes: every
+ * wait bounded by timeout_ms (1 .. 10000), the first K tile of each CTA never
+ * loaded.
+ */
+int parallax_testing_prefill_paged_stalled(
+    const void* q, const void* r, const void* k_pages, const void* v_pages,
+    const int32_t* block_table, const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
+    void* out, int B, int total_tokens, int Hq, int Hkv, int D, float scale, int causal,
+    void* stream, int num_pages, int page_size, int max_pages_per_seq, int probe, void* workspace,
+    size_t workspace_bytes, int timeout_ms);
+
 #ifdef __cplusplus
 }
 #endif

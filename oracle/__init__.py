@@ -201,6 +201,40 @@ class Oracle:
         lens = np.array([len(x) for x in rows], dtype=np.int32)
         return self._decode(q, r, kg, vg, lens, scale, probe)
 
+    def parallax_prefill_paged(self, q, r, k_pages, v_pages, block_table, cu_seqlens_q, seqlens,
+                               scale, causal=True, probe=True):
+        """Chunk attention over a paged cache: q, r [total, Hq, D], sequence b's
+        c rows cu_seqlens_q[b]:cu_seqlens_q[b+1] are the last of its n =
+        seqlens[b] keys. Row j is row n - c + j of the prefill over the gathered
+        keys (rows before the chunk are filled with zeros and dropped); a causal
+        row before the first key is 0. r = 0 gives softmax attention."""
+        q, kp, vp = _f64(q), _f64(k_pages), _f64(v_pages)
+        r = _f64(r) if probe else np.zeros_like(q)
+        host = lambda x: np.asarray(x.cpu() if hasattr(x, "cpu") else x).astype(np.int64)
+        table, cu, lens = host(block_table), host(cu_seqlens_q), host(seqlens)
+        ps = kp.shape[1]
+        out = np.zeros_like(q)
+        for b in range(len(lens)):
+            a, e, n = int(cu[b]), int(cu[b + 1]), int(lens[b])
+            if e == a or n == 0:
+                continue
+            i = np.arange(n)
+            page, slot = table[b, i // ps], i % ps
+            k, v = (x[page, slot].transpose(1, 0, 2)[None] for x in (kp, vp))
+            # rows of the chunk that exist as rows of an n-row prefill; without
+            # the causal mask every row is the same query over all keys
+            for lo in range(a, e, n):
+                hi = min(e, lo + n)
+                if causal:
+                    lo, hi = max(a, e - n), e
+                pad = lambda x: np.concatenate(
+                    [np.zeros((n - (hi - lo),) + x.shape[1:]), x[lo:hi]]).transpose(1, 0, 2)[None]
+                o = self.parallax_prefill(pad(q), pad(r), k, v, scale, causal)
+                out[lo:hi] = o[0].transpose(1, 0, 2)[n - (hi - lo):]
+                if causal:
+                    break
+        return out
+
     # The default used by parity checks: the definition (covariance) form.
     def parallax_decode(self, q, r, k, v, seqlens, scale):
         return self.parallax_covariance(q, r, k, v, seqlens, scale)
@@ -253,6 +287,10 @@ def parallax_decode_paged(*a, **kw):
 
 def parallax_decode_block_sparse(*a, **kw):
     return default().parallax_decode_block_sparse(*a, **kw)
+
+
+def parallax_prefill_paged(*a, **kw):
+    return default().parallax_prefill_paged(*a, **kw)
 
 
 def num_threads() -> int:

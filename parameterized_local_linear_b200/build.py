@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libparallax.so")
-SOURCES = [os.path.join(CSRC, "parallax_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("parallax_api.cu", "norm_rope_api.cu", "chunk_api.cu")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
@@ -32,7 +32,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
-           "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
+           "-std=c++17", "-t", "0", "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
            "-o", LIB + ".tmp", *SOURCES]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -1,0 +1,200 @@
+// How the chunk attention over a paged cache is dealt to its CTAs; shared by
+// the attention kernel and its merge kernel.
+//
+// A row tile is `tpt` consecutive new tokens of one sequence with all G query
+// heads of one kv head (tpt = 128 / G, so at most 128 rows); an item is a row
+// tile and a kv head. It walks the 64-key tiles its last row can see, at least
+// one (a masked one, if it sees no key: its rows are then written as zeros).
+// The items are laid end to end, ordered by (sequence, kv head, row tile), each
+// kChunkItemCost + tiles long: the fixed part stands for the tiles' worth of
+// time that loading Q and R and writing the result take. P CTAs cut the line
+// into equal ranges, so whatever the lengths, every CTA gets the same work and
+// the last key of a long row tile does not leave one CTA running alone. The
+// part of an item inside a range is a piece; a piece that does not hold all of
+// its item's tiles writes a partial record to slot 2c (a piece at the start of
+// range c) or 2c + 1 (one at its end), and the CTA in whose range the item ends
+// merges them.
+#pragma once
+
+#include <cstdint>
+
+#include "partition.cuh"
+
+namespace plx {
+
+constexpr int kChunkRows = 128;
+constexpr int kChunkKeys = 64;
+constexpr int kChunkItemCost = 3;
+
+struct ChunkSpace {
+  const int32_t* cu;    // [B + 1] first new token of each sequence
+  const int32_t* lens;  // [B] cached keys, the new tokens' included
+  int B, total, Lmax, Hkv, tpt, causal;
+};
+
+struct ChunkSeq {
+  int s0, q, n;  // first packed row, new tokens, cached keys
+};
+
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
+  ChunkSeq s;
+  s.s0 = min(max(__ldg(sp.cu + b), 0), sp.total);
+  s.q = min(max(__ldg(sp.cu + b + 1), s.s0), sp.total) - s.s0;
+  s.n = clamp_len(__ldg(sp.lens + b), sp.Lmax);
+  return s;
+}
+
+// A sequence whose bounds or length chunk_seq clamped, or with more new tokens
+// than keys.
+__device__ __forceinline__ bool chunk_seq_clamped(const ChunkSpace& sp, int b) {
+  const int a = __ldg(sp.cu + b), e = __ldg(sp.cu + b + 1), n = __ldg(sp.lens + b);
+  return a < 0 || e < a || e > sp.total || n < 0 || n > sp.Lmax || (sp.causal && n < e - a);
+}
+
+// Keys the last row of row tile rt sees, and the tiles that hold them.
+__device__ __forceinline__ int chunk_kend(const ChunkSpace& sp, const ChunkSeq& s, int rt) {
+  if (!sp.causal) return s.n;
+  const int last = rt < s.q / sp.tpt ? (rt + 1) * sp.tpt : s.q;  // tokens up to this tile's end
+  return max(0, s.n - s.q + last);
+}
+__device__ __forceinline__ int chunk_tiles(const ChunkSpace& sp, const ChunkSeq& s, int rt) {
+  return max(1, (chunk_kend(sp, s, rt) + kChunkKeys - 1) / kChunkKeys);
+}
+__device__ __forceinline__ int chunk_row_tiles(const ChunkSpace& sp, const ChunkSeq& s) {
+  return (s.q + sp.tpt - 1) / sp.tpt;
+}
+// The length of one kv head's items of a sequence.
+__device__ __forceinline__ long long chunk_seq_cost(const ChunkSpace& sp, const ChunkSeq& s) {
+  const int nrt = chunk_row_tiles(sp, s);
+  long long c = 0;
+  for (int rt = 0; rt < nrt; ++rt) c += chunk_tiles(sp, s, rt) + kChunkItemCost;
+  return c;
+}
+
+struct ChunkRange {
+  long long per, lo, hi;  // this CTA's range [lo, hi) of the line
+  int b, g, rt;           // the item at lo (valid if lo < hi)
+  int off;                // lo's offset in it
+  ChunkSeq s;
+  int clamped;
+};
+
+// Warp-cooperative, no barrier: each lane sums a contiguous chunk of the
+// sequences, a scan gives the prefix, and the lane whose chunk holds lo walks
+// to the item there.
+__device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
+  const int lane = threadIdx.x & 31;
+  const int chunk = (sp.B + 31) / 32;
+  const int b0 = min(sp.B, lane * chunk), b1 = min(sp.B, b0 + chunk);
+  long long local = 0;
+  int clamped = 0;
+  for (int b = b0; b < b1; ++b) {
+    clamped |= chunk_seq_clamped(sp, b);
+    local += chunk_seq_cost(sp, chunk_seq(sp, b)) * sp.Hkv;
+  }
+  long long incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  ChunkRange r{};
+  r.clamped = __any_sync(0xffffffffu, clamped);
+  const long long total = __shfl_sync(0xffffffffu, incl, 31);
+  // at least one tile past the fixed part, so that no range is all overhead
+  r.per = max((long long)kChunkItemCost + 1, div_pos(total + P - 1, P));
+  r.lo = min(total, (long long)c * r.per);
+  r.hi = min(total, r.lo + r.per);
+  long long pos = incl - local;
+  int fb = -1, fg = 0, frt = 0, foff = 0;
+  if (r.lo < r.hi && r.lo >= pos && r.lo < incl) {
+    for (int b = b0; b < b1; ++b) {
+      const ChunkSeq s = chunk_seq(sp, b);
+      const long long w = chunk_seq_cost(sp, s);
+      if (r.lo < pos + w * sp.Hkv) {
+        long long rem = r.lo - pos;
+        fb = b;
+        fg = (int)div_pos(rem, w);
+        rem -= w * fg;
+        const int nrt = chunk_row_tiles(sp, s);
+        for (; frt + 1 < nrt; ++frt) {
+          const int len = chunk_tiles(sp, s, frt) + kChunkItemCost;
+          if (rem < len) break;
+          rem -= len;
+        }
+        foff = (int)rem;
+        break;
+      }
+      pos += w * sp.Hkv;
+    }
+  }
+  const unsigned owner = __ballot_sync(0xffffffffu, fb >= 0);
+  if (owner) {
+    const int src = __ffs(owner) - 1;
+    r.b = __shfl_sync(0xffffffffu, fb, src);
+    r.g = __shfl_sync(0xffffffffu, fg, src);
+    r.rt = __shfl_sync(0xffffffffu, frt, src);
+    r.off = __shfl_sync(0xffffffffu, foff, src);
+    r.s = chunk_seq(sp, r.b);
+  }
+  return r;
+}
+
+struct ChunkPiece {
+  int b, g, rt;
+  int t0, t1;     // its tiles
+  bool complete;  // all of the item's tiles
+  bool first;     // at the start of the CTA's range
+  ChunkSeq s;
+};
+
+// Walks the pieces of one range; every role of a CTA walks the same list.
+struct ChunkCursor {
+  long long pos, lo, hi;
+  int b, g, rt, off;
+  ChunkSeq s;
+
+  __device__ explicit ChunkCursor(const ChunkRange& r)
+      : pos(r.lo), lo(r.lo), hi(r.hi), b(r.b), g(r.g), rt(r.rt), off(r.off), s(r.s) {}
+
+  __device__ bool next(const ChunkSpace& sp, ChunkPiece& pc) {
+    while (pos < hi) {
+      const int nt = chunk_tiles(sp, s, rt), len = nt + kChunkItemCost;
+      const int take = (int)min((long long)(len - off), hi - pos);
+      pc.b = b;
+      pc.g = g;
+      pc.rt = rt;
+      pc.s = s;
+      pc.t0 = max(0, off - kChunkItemCost);
+      pc.t1 = max(0, off + take - kChunkItemCost);
+      pc.complete = pc.t0 == 0 && pc.t1 == nt;
+      pc.first = pos == lo;
+      pos += take;
+      off += take;
+      if (off == len) {
+        off = 0;
+        if (++rt == chunk_row_tiles(sp, s)) {
+          rt = 0;
+          if (++g == sp.Hkv) {
+            g = 0;
+            do {
+              if (pos >= hi || ++b >= sp.B) {
+                hi = pos;  // past the last item
+                break;
+              }
+              s = chunk_seq(sp, b);
+            } while (s.q == 0);
+          }
+        }
+      }
+      if (pc.t1 > pc.t0) return true;
+    }
+    return false;
+  }
+};
+
+// A partial record: m, l, b of the 128 rows, then A and C as [D / 4][128 rows]
+// float4, so that a warp's rows are contiguous when written and when merged.
+__host__ __device__ constexpr int chunk_rec_floats(int D) { return kChunkRows * (4 + 2 * D); }
+
+}  // namespace plx

@@ -3,7 +3,6 @@
 // The host never synchronises and never allocates; every launch goes to the
 // caller's stream.
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
@@ -18,6 +17,7 @@
 #include "parallax_testing.h"
 
 #include "common.cuh"
+#include "host.cuh"
 #include "kernel_cluster.cuh"
 #include "kernel_copy.cuh"
 #include "kernel_generic.cuh"
@@ -60,29 +60,6 @@ struct Call {
   const int32_t* num_blocks;
   int page_size, num_pages;
 };
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// SM count of the current device, cached per device (host threads may call
-// concurrently: the cache entries are atomics).
-int current_sm_count(int* out) {
-  static std::atomic<int> cache[256];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PARALLAX_ERR_CUDA;
-  if (dev >= 0 && dev < 256) {
-    const int n = cache[dev].load(std::memory_order_relaxed);
-    if (n > 0) {
-      *out = n;
-      return PARALLAX_OK;
-    }
-  }
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    return PARALLAX_ERR_CUDA;
-  if (dev >= 0 && dev < 256) cache[dev].store(n, std::memory_order_relaxed);
-  *out = n;
-  return PARALLAX_OK;
-}
 
 // PARALLAX_SPLITS (a positive integer, read once per process) overrides the
 // split heuristic, for experiments; 0 when unset or invalid.
@@ -184,67 +161,7 @@ int validate(const Call& c) {
   return PARALLAX_OK;
 }
 
-// --------------------------------------------------------- TMA descriptors --
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-// Element strides of (batch row, kv head, key) in a cache of either layout.
-struct KvStrides {
-  long long b, h, k;
-};
-KvStrides kv_strides(int layout, int Hkv, int Lmax, int D) {
-  if (layout == PARALLAX_KV_BSHD)
-    return {(long long)Lmax * Hkv * D, (long long)D, (long long)Hkv * D};
-  return {(long long)Hkv * Lmax * D, (long long)Lmax * D, (long long)D};
-}
-
-// A bf16 cache of either layout viewed as {64 dims, Lmax keys, D/64 halves,
-// Hkv heads, B rows}: one box of 64 keys x D dims lands as D/64 swizzled
-// [64 keys][128 bytes] blocks, one per 64-dim half.
-int encode_cache_map(CUtensorMap* map, const void* cache, int D, int Lmax, int Hkv, int B,
-                     int layout) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return PARALLAX_ERR_CUDA;
-  const KvStrides st = kv_strides(layout, Hkv, Lmax, D);
-  cuuint64_t dims[5] = {64, (cuuint64_t)Lmax, (cuuint64_t)(D / 64), (cuuint64_t)Hkv,
-                        (cuuint64_t)B};
-  cuuint64_t strides[4] = {(cuuint64_t)st.k * 2, 128, (cuuint64_t)st.h * 2, (cuuint64_t)st.b * 2};
-  cuuint32_t box[5] = {64, (cuuint32_t)kTileKeys, (cuuint32_t)(D / 64), 1, 1};
-  cuuint32_t elem[5] = {1, 1, 1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(cache), dims,
-                   strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? PARALLAX_OK : PARALLAX_ERR_CUDA;
-}
-
 // ----------------------------------------------------------------- launch --
-
-// Raises the kernel's dynamic shared-memory limit once per device (the
-// attribute call is idempotent, so two threads racing here both succeed).
-template <typename Kernel>
-int set_smem_once(Kernel kernel, int bytes, std::atomic<int>* done_dev) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PARALLAX_ERR_CUDA;
-  if (dev >= 0 && dev < 256 && done_dev[dev].load(std::memory_order_acquire) >= bytes)
-    return PARALLAX_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess)
-    return PARALLAX_ERR_CUDA;
-  if (dev >= 0 && dev < 256) done_dev[dev].store(bytes, std::memory_order_release);
-  return PARALLAX_OK;
-}
 
 template <int D, bool PROBE, bool OUT_F32>
 int launch_tc(const Call& c, const DecodeParams& prm, int P) {
@@ -801,6 +718,7 @@ int parallax_workspace_status(void* workspace, int clear, uint32_t* device_statu
   *device_status = word;
   if (word & PARALLAX_DEVICE_STATUS_TIMEOUT) return PARALLAX_ERR_DEVICE_TIMEOUT;
   if (word & PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED) return PARALLAX_ERR_SEQLEN_CLAMPED;
+  if (word & PARALLAX_DEVICE_STATUS_POSITION_CLAMPED) return PARALLAX_ERR_POSITION_CLAMPED;
   return PARALLAX_OK;
 }
 
@@ -818,6 +736,8 @@ const char* parallax_status_string(int status) {
     case PARALLAX_ERR_DEVICE_TIMEOUT: return "a bounded wait inside a kernel timed out";
     case PARALLAX_ERR_BAD_PHASE: return "phase must be 1 or 2";
     case PARALLAX_ERR_SEQLEN_CLAMPED: return "a cache_seqlens value was outside [0, Lmax] and was clamped";
+    case PARALLAX_ERR_POSITION_CLAMPED:
+      return "a rotary position was outside [0, max_positions) and was clamped";
     case PARALLAX_ERR_SCRATCH_LIMIT:
       return "the workspace this call needs exceeds PARALLAX_NOALLOC_SCRATCH_BYTES (lower num_splits)";
     default: return "unknown status";

@@ -1,0 +1,291 @@
+"""GPU tests of the chunk attention over a paged cache (parallax_prefill_paged)
+against the definition in 64 bits.
+
+Tolerance of an output o_d: half a bf16 step, 2^-8 |o_d|, plus a share of
+S_d = sum_i w_i (1 + |s_i - sbar|) (|v_id| + |vbar_d|), the size of the terms it
+is summed from. The share: a weight's rounding to 17 bits twice (2^-17), the
+scores' error (8 accumulation steps of 2^-23 over sums that reach 10 in the
+exponent and 80 in s: 1.2e-5 + 8e-5), and the value products' accumulator, off by
+at most 2^-23 a step in 16 keys / 4 products: 6e-8 per two keys. 2e-4 + 6e-8 n
+covers them at n keys."""
+import pytest
+import torch
+
+import oracle
+from parameterized_local_linear_b200 import binding as pl
+from test_gpu_norm_rope import inputs as rope_inputs
+from test_gpu_norm_rope import make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(q, r, kp, vp, table, cu, lens, causal, scale):
+    """(o, S) in fp64, row by row from the definition; untouched rows stay NaN."""
+    G = q.shape[1] // kp.shape[2]
+    ps, D = kp.shape[1], q.shape[2]
+    o = torch.full(q.shape, float("nan"), dtype=torch.float64, device="cuda")
+    S = torch.zeros_like(o)
+    for b in range(len(lens)):
+        a, e, n = int(cu[b]), int(cu[b + 1]), int(lens[b])
+        if e == a:
+            continue
+        i = torch.arange(n, device="cuda")
+        page = table[b].long()[i // ps]
+        ok = (page >= 0) & (page < kp.shape[0])
+        page = page.clamp(0, kp.shape[0] - 1)
+        k, v = (torch.where(ok[:, None, None], x[page, i % ps].double(), 0.0)
+                .repeat_interleave(G, 1).transpose(0, 1) for x in (kp, vp))  # [Hq, n, D]
+        qq = q[a:e].double().transpose(0, 1)
+        c = e - a
+        seen = ok[None, :] & (i[None, :] <= (torch.arange(c, device="cuda") + n - c)[:, None]
+                              if causal else torch.ones(c, n, device="cuda", dtype=torch.bool))
+        t = (qq @ k.transpose(1, 2) * scale).masked_fill(~seen, float("-inf"))
+        w = torch.softmax(t, -1).nan_to_num(0.0)
+        vbar = w @ v
+        s = torch.zeros_like(w) if r is None else r[a:e].double().transpose(0, 1) @ k.transpose(1, 2)
+        dev = s - (w * s).sum(-1, keepdim=True)
+        o[a:e] = (vbar + (w * dev) @ v - (w * dev).sum(-1, keepdim=True) * vbar).transpose(0, 1)
+        ww = w * (1 + dev.abs())
+        S[a:e] = (ww @ v.abs() + ww.sum(-1, keepdim=True) * vbar.abs()).transpose(0, 1)
+    return o, S
+
+
+def check(got, o, S, nmax, what=()):
+    assert got.dtype == torch.bfloat16
+    rows = ~o.isnan().all(-1).all(-1)
+    err = (got.double() - o).abs()[rows]
+    tol = (2.0 ** -8 * o.abs() + (2e-4 + 6e-8 * nmax) * S)[rows]
+    bad = ~(err <= tol)
+    assert not bad.any(), (what, err[bad].max().item(), (err / tol.clamp_min(1e-30)).max().item())
+
+
+def make(seqs, ps, Hq, Hkv, D, seed, pad=0, poison=True, r_scale=0.5):
+    kp, vp, table, cu, lens = make_cache(seqs, ps, Hkv, D, torch.bfloat16, seed)
+    n = int(cu[-1]) + pad
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn(max(n, 1), Hq, D, device="cuda", generator=g).bfloat16()
+    r = (torch.randn(max(n, 1), Hq, D, device="cuda", generator=g) * r_scale).bfloat16()
+    if poison:  # every slot that no key fills
+        used = torch.zeros(kp.shape[:2], dtype=torch.bool)
+        for b, (_, m) in enumerate(seqs):
+            i = torch.arange(m)
+            used[table[b].cpu().long()[i // ps], i % ps] = True
+        kp[~used.cuda()] = float("nan")
+        vp[~used.cuda()] = float("nan")
+    return q, r, kp, vp, table, cu, lens
+
+
+SHAPES = [
+    [(1, 1)],
+    [(1, 64)],
+    [(2, 65), (64, 64), (1, 63)],
+    [(5, 5), (0, 70), (130, 200), (0, 0), (1, 129), (65, 300)],
+    [(3, 700), (200, 1000)],
+    [(1, 130)] * 40,
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 16, 8), (128, 2, 2), (64, 8, 2), (64, 3, 1)])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_matches_definition(shape, D, Hq, Hkv, causal):
+    seqs = SHAPES[shape]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64 if shape % 2 else 128, Hq, Hkv, D, 70 + shape)
+    scale = D ** -0.5
+    for probe in (True, False):
+        ws = pl.prefill_paged_workspace(len(seqs), q.shape[0], Hq, Hkv, D, q.device)
+        got = pl.parallax_prefill_paged(q, r if probe else None, kp, vp, table, lens, cu,
+                                        causal=causal, probe=probe, workspace=ws)
+        o, S = reference(q, r if probe else None, kp, vp, table, cu, lens, causal, scale)
+        check(got, o, S, max(n for _, n in seqs), (seqs, D, probe))
+        assert int(ws[:4].view(torch.int32)) == 0
+        again = pl.parallax_prefill_paged(q, r if probe else None, kp, vp, table, lens, cu,
+                                          causal=causal, probe=probe, workspace=ws)
+        assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("r_scale", [0.0, 1.0, 2.0])
+def test_probe_scales_and_oracle(r_scale):
+    seqs = [(33, 150), (4, 4)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, 128, 80, r_scale=r_scale)
+    got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, scale=0.07)
+    o, S = reference(q, r, kp, vp, table, cu, lens, True, 0.07)
+    check(got, o, S, 150)
+    want = oracle.parallax_prefill_paged(q, r, kp, vp, table, cu, lens, 0.07)
+    assert abs(o.cpu().numpy() - want).max() <= 1e-9
+
+
+@pytest.mark.parametrize("G,D", [(5, 64), (8, 128), (16, 64), (128, 64)])
+def test_large_and_odd_groups(G, D):
+    seqs = [(3, 70), (140, 260), (1, 1)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 2 * G, 2, D, 85)
+    got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu)
+    o, S = reference(q, r, kp, vp, table, cu, lens, True, D ** -0.5)
+    check(got, o, S, 260, G)
+
+
+def test_long_context_is_split_and_merged():
+    """One kv head, few rows: every CTA holds a part of each item."""
+    for seqs in ([(4, 20000)], [(64, 9001)], [(300, 5000), (1, 12345)]):
+        q, r, kp, vp, table, cu, lens = make(seqs, 256, 2, 1, 128, 90)
+        got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu)
+        o, S = reference(q, r, kp, vp, table, cu, lens, True, 128 ** -0.5)
+        check(got, o, S, max(n for _, n in seqs), seqs)
+
+
+def test_large_scores_and_offsets():
+    """Keys with a common offset (large s and t with small spread) and logits
+    that grow along the row, so that the running maximum is rescaled often."""
+    seqs = [(40, 400)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, 64, 95, poison=False)
+    i = torch.arange(400, device="cuda")
+    page, slot = table[0].long()[i // 64], i % 64
+    kp[page, slot] = (kp[page, slot].float() * (0.02 * i[:, None, None] + 0.1) + 1.0).bfloat16()
+    got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, scale=0.5)
+    o, S = reference(q, r, kp, vp, table, cu, lens, True, 0.5)
+    # scores up to 40 times those of the tolerance's derivation
+    err = (got.double() - o).abs()
+    assert (err <= 2.0 ** -8 * o.abs() + 40 * 2e-4 * S).all()
+
+
+def test_rows_without_keys_padding_and_bad_pages():
+    seqs = [(6, 4), (3, 0), (2, 130), (70, 100)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, 128, 97, pad=11)
+    out = torch.full_like(q, 5.0)
+    ws = pl.prefill_paged_workspace(4, q.shape[0], 4, 2, 128, q.device)
+    run = lambda t, n, c=cu: pl.parallax_prefill_paged(q, r, kp, vp, t, n, c, out=out, workspace=ws)
+    run(table, lens)
+    o, S = reference(q, r, kp, vp, table, cu, lens, True, 128 ** -0.5)
+    check(out, o, S, 130)
+    assert (out[:2] == 0).all() and (out[6:9] == 0).all()  # no key seen
+    assert (out[int(cu[-1]):] == 5).all()                  # rows past the last sequence
+    assert int(ws[:4].view(torch.int32)) == 2              # more new tokens than keys
+    # a page outside the pool is left out
+    for bad in (-1, kp.shape[0], 2 ** 31 - 1):
+        t = table.clone()
+        t[3, 0] = bad
+        ws.zero_()
+        run(t, lens)
+        o, S = reference(q, r, kp, vp, t, cu, lens, True, 128 ** -0.5)
+        check(out, o, S, 130, bad)
+        assert int(ws[:4].view(torch.int32)) == 2
+    # a length past the table, a negative one: clamped
+    n2 = lens.clone()
+    n2[2], n2[0] = 10 ** 6, -5
+    kp2, vp2 = kp.nan_to_num(0.5), vp.nan_to_num(0.5)
+    t = table.clamp_min(0)
+    ws.zero_()
+    pl.parallax_prefill_paged(q, r, kp2, vp2, t, n2, cu, out=out, workspace=ws)
+    fixed = n2.clamp(0, 64 * t.shape[1])
+    o, S = reference(q, r, kp2, vp2, t, cu, fixed, True, 128 ** -0.5)
+    check(out, o, S, 256)
+    assert int(ws[:4].view(torch.int32)) == 2
+
+
+def test_malformed_cu_seqlens_stays_in_bounds():
+    seqs = [(10, 70), (20, 90), (5, 40)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, 64, 98, poison=False)
+    ws = pl.prefill_paged_workspace(3, q.shape[0], 4, 2, 64, q.device)
+    bad = torch.tensor([-3, 12, 9, 1000], dtype=torch.int32, device="cuda")
+    got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, bad, workspace=ws)
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(torch.int32)) == 2 and got.isfinite().all()
+
+
+def test_one_token_form_is_the_decode():
+    seqs = [(1, 300), (1, 1), (1, 64), (1, 129)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 16, 8, 128, 99, poison=False)
+    t = table.clamp_min(0)
+    a = pl.parallax_prefill_paged(q, r, kp, vp, t, lens)
+    b = pl.parallax_decode_paged(q, r, kp, vp, t, lens)
+    assert torch.equal(a, b)
+    o, S = reference(q, r, kp, vp, t, cu, lens, True, 128 ** -0.5)
+    check(a, o, S, 300)
+    check(pl.parallax_prefill_paged(q, r, kp, vp, t, lens, cu), o, S, 300)
+
+
+def test_streams_and_two_graphs():
+    seqs = [(30, 500), (1, 90)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, 128, 101)
+    want = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, stream=s)
+    s.synchronize()
+    assert torch.equal(want, got)
+    graphs = []
+    for _ in range(2):
+        ws = pl.prefill_paged_workspace(2, q.shape[0], 4, 2, 128, q.device)
+        out = torch.zeros_like(q)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, out=out, workspace=ws)
+        graphs.append((graph, out, ws))  # a graph's workspace lives as long as the graph
+    for graph, *_ in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, out) for _, out, _ in graphs)
+
+
+def test_bounded_wait_reports_and_context_survives():
+    """The producer never loads the first K tile: the waits run out, the status
+    word says so, and the next call is right."""
+    import ctypes
+    seqs = [(30, 500)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, 128, 103)
+    ws = pl.prefill_paged_workspace(1, 30, 4, 2, 128, q.device)
+    out = torch.zeros_like(q)
+    fn = pl.load_library().parallax_testing_prefill_paged_stalled
+    i, vp_, f = ctypes.c_int, ctypes.c_void_p, ctypes.c_float
+    fn.argtypes = [vp_] * 8 + [i] * 5 + [f, i, vp_] + [i] * 4 + [vp_, ctypes.c_size_t, i]
+    fn.restype = i
+    rc = fn(q.data_ptr(), r.data_ptr(), kp.data_ptr(), vp.data_ptr(), table.data_ptr(),
+            cu.data_ptr(), lens.data_ptr(), out.data_ptr(), 1, 30, 4, 2, 128, 0.1, 1,
+            torch.cuda.current_stream().cuda_stream, kp.shape[0], 64, table.shape[1], 1,
+            ws.data_ptr(), ws.numel(), 50)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert int(ws[:4].view(torch.int32)) & 1
+    ws[:256].zero_()
+    got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, workspace=ws)
+    o, S = reference(q, r, kp, vp, table, cu, lens, True, 128 ** -0.5)
+    check(got, o, S, 500)
+    assert int(ws[:4].view(torch.int32)) == 0
+
+
+def test_serving_run_together():
+    """Prompts in chunks, then decode steps, through append, chunk attention and
+    decode over one pool, against one pass over the whole sequences in 64 bits
+    (on the bf16 rows that the norm and rotation gave, which have their own tests)."""
+    Hq, Hkv, D, ps, total = 8, 4, 128, 64, [150, 64, 9]
+    B = len(total)
+    (q, r, k, v), w, _, cs = rope_inputs(sum(total), Hq, Hkv, D, D, torch.bfloat16, 110)
+    start = torch.tensor([0, *total]).cumsum(0)[:-1]
+    kp, vp, table, _, _ = make_cache([(0, n) for n in total], ps, Hkv, D, torch.bfloat16, 111)
+    kp.fill_(float("nan")), vp.fill_(float("nan"))
+    pos = torch.cat([torch.arange(n) for n in total]).int().cuda()
+    fq, fr, fk = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w)
+    done = [0] * B
+    ws = pl.prefill_paged_workspace(B, sum(total), Hq, Hkv, D, q.device)
+    out = torch.zeros_like(q[:, :Hq]).contiguous()
+    for step in ([70, 1, 8], [79, 62, 0], [1, 1, 1]):
+        rows = torch.cat([start[b] + torch.arange(done[b], done[b] + c) for b, c in enumerate(step)]).cuda()
+        done = [d + c for d, c in zip(done, step)]
+        cu = torch.tensor([0, *step]).cumsum(0).int().cuda()
+        lens = torch.tensor(done, dtype=torch.int32, device="cuda")
+        one = all(c == 1 for c in step)
+        a, b = pl.parallax_norm_rope_append(q[rows], r[rows], k[rows], v[rows], cs, kp, vp, table,
+                                            lens, None if one else cu, None, *w)
+        out[rows] = pl.parallax_prefill_paged(a, b, kp, vp, table, lens, None if one else cu,
+                                              workspace=ws)
+    cu = torch.tensor([0, *total]).cumsum(0).int().cuda()
+    o = torch.zeros(sum(total), Hq, D, dtype=torch.float64, device="cuda")
+    lens = torch.tensor(total, dtype=torch.int32, device="cuda")
+    fkp, fvp = torch.zeros_like(kp), torch.zeros_like(vp)
+    for b, n in enumerate(total):
+        i = torch.arange(n, device="cuda")
+        fkp[table[b].long()[i // ps], i % ps] = fk[int(start[b]):int(start[b]) + n]
+        fvp[table[b].long()[i // ps], i % ps] = v[int(start[b]):int(start[b]) + n]
+    o, S = reference(fq, fr, fkp, fvp, table, cu, lens, True, D ** -0.5)
+    # normed, weighted probe rows: |r| about 1 per dimension and s up to 60
+    check(out, o, 3 * S, max(total))

@@ -1,0 +1,343 @@
+"""GPU tests of the norm and rotation of the heads (parallax_qk_norm_rope, its
+backward pass and parallax_norm_rope_append) against the formulas in 64 bits.
+
+Tolerances count roundings (u = 2^-24 of fp32, half a step of the output type):
+a value n = x rstd w carries at most 20 u (the sum of squares of 128 values in 16
+serial and 3 or 2 tree steps, its root and reciprocal, two products), and the
+rotation adds two products and a sum: 24 u of |n_a| + |n_b| in all. A row gradient
+is rstd (dn - xh mean(dn xh)) with two such sums: 48 u of rstd (|dn| + |xh|
+mean|dn xh|). A weight gradient adds at most 60 terms one after the other at
+these sizes (a lane's rows, the lanes, warps and blocks), each within 30 u:
+90 u of sum |dz xh|."""
+import pytest
+import torch
+
+from parameterized_local_linear_b200 import binding as pl
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+EPS = 1e-6
+
+
+def rotate(y, cs, interleaved, sign=1.0):
+    h = cs.shape[1] // 2
+    cos, sin = cs[:, None, :h], sign * cs[:, None, h:]
+    ia = torch.arange(h, device=y.device) * (2 if interleaved else 1)
+    ib = ia + (1 if interleaved else h)
+    out = y.clone()
+    out[..., ia] = y[..., ia] * cos - y[..., ib] * sin
+    out[..., ib] = y[..., ia] * sin + y[..., ib] * cos
+    return out
+
+
+def spread(y, rot, interleaved):
+    """|y_a| + |y_b| of each dimension's pair (|y| past rot)."""
+    h = rot // 2
+    ia = torch.arange(h, device=y.device) * (2 if interleaved else 1)
+    ib = ia + (1 if interleaved else h)
+    out = y.abs().clone()
+    out[..., ia] = out[..., ib] = y[..., ia].abs() + y[..., ib].abs()
+    return out
+
+
+def normed(x, w):
+    x = x.double()
+    return x if w is None else x / torch.sqrt(x.square().mean(-1, keepdim=True) + EPS) * w.double()
+
+
+def check(got, want, slack, dtype, what):
+    err = (got.double() - want).abs()
+    tol = HALF[dtype] * want.abs() + slack
+    assert got.dtype == dtype and got.shape == want.shape
+    bad = ~(err <= tol)
+    assert not bad.any(), (what, err[bad].max().item(), (err / tol.clamp_min(1e-300)).max().item())
+
+
+def layout(y, L):
+    return y.unflatten(0, (-1, L)).transpose(1, 2).contiguous() if L else y
+
+
+def inputs(n, Hq, Hkv, D, rot, dtype, seed, npos=4096, fused=True, r=True, v=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    heads = [Hq, Hq, Hkv, Hkv]
+    x = (torch.randn(n, sum(heads), D, device="cuda", generator=g) * 2).to(dtype)
+    parts = list(x.split(heads, 1)) if fused else [p.contiguous() for p in x.split(heads, 1)]
+    w = [(1 + 0.3 * torch.randn(D, device="cuda", generator=g)).to(dtype) for _ in range(3)]
+    pos = torch.randint(0, npos, (n,), device="cuda", generator=g, dtype=torch.int32)
+    cs = pl.parallax_rope_table(npos, rot, 1e4)
+    return (parts if r else [parts[0], None, *parts[2:]]), w, pos, cs
+
+
+@pytest.mark.parametrize("rot", [16, 64, 96, 128])
+def test_table(rot):
+    cs = pl.parallax_rope_table(70000, rot, 1e6)
+    t = torch.arange(70000, dtype=torch.float64, device="cuda")[:, None]
+    ang = t * 1e6 ** (-torch.arange(0, rot, 2, dtype=torch.float64, device="cuda") / rot)
+    want = torch.cat([ang.cos(), ang.sin()], 1)
+    # the angle in fp64: 70000 x 2^-53 times a few steps, then half a step of fp32
+    assert ((cs.double() - want).abs() <= U * want.abs() + 1e-10).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 96), (128, 16), (64, 64), (64, 32)])
+@pytest.mark.parametrize("n,Hq,Hkv", [(1, 1, 1), (7, 6, 2), (50, 16, 8), (500, 16, 8)])
+def test_forward(n, Hq, Hkv, D, rot, interleaved, dtype):
+    (q, r, k, _), w, pos, cs = inputs(n, Hq, Hkv, D, rot, dtype, seed=n + rot)
+    for weights, probe in ((w, True), ([w[0], None, w[2]], True), ([None] * 3, False)):
+        got = pl.parallax_qk_norm_rope(q, r if probe else None, k, cs, pos, *weights,
+                                       interleaved=interleaved)
+        assert (got[1] is None) == (not probe)
+        for x, wt, o in zip((q, r, k), weights, got):
+            if o is None:
+                continue
+            y = normed(x, wt)
+            check(o, rotate(y, cs[pos.long()].double(), interleaved),
+                  24 * U * spread(y, rot, interleaved), dtype, (n, D, rot, wt is None))
+
+
+@pytest.mark.parametrize("L", [1, 5, 40])
+def test_batched_layout_and_default_positions(L):
+    n, Hq, Hkv, D = 3 * L, 4, 2, 128
+    (q, r, k, _), w, _, cs = inputs(n, Hq, Hkv, D, 128, torch.bfloat16, seed=L)
+    pos = torch.arange(n, device="cuda", dtype=torch.int32) % L
+    flat = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w)
+    got = pl.parallax_qk_norm_rope(q, r, k, cs, None, *w, seq_len=L)
+    for a, b in zip(flat, got):
+        assert torch.equal(layout(a, L), b)
+    # packed without positions: 0, 1, ...
+    a = pl.parallax_qk_norm_rope(q, r, k, cs, None, *w)
+    b = pl.parallax_qk_norm_rope(q, r, k, cs, torch.arange(n, device="cuda", dtype=torch.int32), *w)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_in_place_and_given_outputs():
+    (q, r, k, _), w, pos, cs = inputs(65, 4, 2, 64, 64, torch.bfloat16, seed=3, fused=False)
+    want = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w)
+    out = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, out=(q, r, k))
+    assert out[0].data_ptr() == q.data_ptr()
+    assert all(torch.equal(a, b) for a, b in zip(want, (q, r, k)))
+
+
+def test_nonfinite_values_stay_in_their_row():
+    (q, r, k, _), w, pos, cs = inputs(9, 4, 2, 128, 64, torch.bfloat16, seed=4)
+    want = pl.parallax_qk_norm_rope(q, r, k, cs, pos, w[0], None, w[2])
+    q[3, 1, 5] = float("nan")
+    r[2, 2, 100] = float("inf")  # no norm, past the rotated dimensions
+    got = pl.parallax_qk_norm_rope(q, r, k, cs, pos, w[0], None, w[2])
+    assert got[0][3, 1].isnan().all()
+    got[0][3, 1] = want[0][3, 1]
+    assert got[1][2, 2, 100] == float("inf")
+    got[1][2, 2, 100] = want[1][2, 2, 100]
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_zero_rows_and_position_clamp():
+    (q, r, k, _), w, pos, cs = inputs(6, 4, 2, 64, 64, torch.float32, seed=5, npos=100)
+    q.zero_()
+    pos[:3] = torch.tensor([-1, 100, 2 ** 31 - 1])
+    ws = pl.status_workspace("cuda")
+    got = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, workspace=ws)
+    assert (got[0] == 0).all()
+    fixed = pos.clamp(0, 99)
+    want = pl.parallax_qk_norm_rope(q, r, k, cs, fixed, *w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert int(ws[:4].view(torch.int32)) == 4
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 32), (64, 64), (64, 48)])
+@pytest.mark.parametrize("n,Hq,Hkv", [(1, 1, 1), (7, 6, 2), (130, 16, 8)])
+def test_backward(n, Hq, Hkv, D, rot, interleaved, dtype):
+    (q, r, k, _), w, pos, cs = inputs(n, Hq, Hkv, D, rot, dtype, seed=n + rot + 1)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dy = [torch.randn(n, H, D, device="cuda", generator=g).to(dtype) for H in (Hq, Hq, Hkv)]
+    c64 = cs[pos.long()].double()
+    for weights, probe in ((w, True), ([w[0], None, w[2]], True), ([None] * 3, False)):
+        got = pl.parallax_qk_norm_rope_backward(dy[0], dy[1] if probe else None, dy[2], q,
+                                                r if probe else None, k, cs, pos, *weights,
+                                                interleaved=interleaved)
+        for i, (x, wt, d) in enumerate(zip((q, r, k), weights, dy)):
+            if i == 1 and not probe:
+                assert got[1] is None and got[4] is None
+                continue
+            dz = rotate(d.double(), c64, interleaved, -1.0)
+            sz = spread(d.double(), rot, interleaved)
+            if wt is None:
+                check(got[i], dz, 4 * U * sz, dtype, "dx")
+                assert got[3 + i] is None
+                continue
+            xd = x.double()
+            rstd = 1 / torch.sqrt(xd.square().mean(-1, keepdim=True) + EPS)
+            xh, dn, sn = xd * rstd, dz * wt.double(), sz * wt.double().abs()
+            dx = rstd * (dn - xh * (dn * xh).mean(-1, keepdim=True))
+            check(got[i], dx, 48 * U * rstd * (sn + xh.abs() * (sn * xh.abs()).mean(-1, keepdim=True)),
+                  dtype, "dx")
+            check(got[3 + i], (dz * xh).sum((0, 1)), 90 * U * (sz * xh.abs()).sum((0, 1)),
+                  torch.float32, "dw")
+
+
+def test_backward_against_differences():
+    """Central differences of the fp64 formula along random directions, and the
+    same of the kernel's own forward (fp32, a large step)."""
+    n, Hq, Hkv, D, rot = 5, 4, 2, 64, 32
+    (q, r, k, _), w, pos, cs = inputs(n, Hq, Hkv, D, rot, torch.float32, seed=21)
+    g = torch.Generator(device="cuda").manual_seed(22)
+    dy = [torch.randn(n, H, D, device="cuda", generator=g) for H in (Hq, Hq, Hkv)]
+    got = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w)
+    c64 = cs[pos.long()].double()
+    for i, (x, wt) in enumerate(zip((q, r, k), w)):
+        dirx = torch.randn(x.shape, device="cuda", generator=g).double()
+        dirw = torch.randn(D, device="cuda", generator=g).double()
+        f = lambda h: (rotate(normed(x.double() + h * dirx, wt.double() + h * dirw), c64, False)
+                       * dy[i].double()).sum()
+        h = 1e-5
+        want = (f(h) - f(-h)) / (2 * h)
+        have = (got[i].double() * dirx).sum() + (got[3 + i].double() * dirw).sum()
+        # 500 terms of order 1, each within 1e-6 of its own; the difference formula
+        # is off by h^2 times the third derivative and 2^-53 / h times the value
+        assert abs(have - want) <= 2e-4 * max(1.0, abs(want)), (i, have, want)
+
+
+def test_backward_layouts_strided_gradients_and_repeat():
+    n, L, Hq, Hkv, D = 60, 20, 4, 2, 128
+    (q, r, k, _), w, _, cs = inputs(n, Hq, Hkv, D, 128, torch.bfloat16, seed=30)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    dy = [torch.randn(n, H, D, device="cuda", generator=g).bfloat16() for H in (Hq, Hq, Hkv)]
+    pos = torch.arange(n, device="cuda", dtype=torch.int32) % L
+    flat = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w)
+    whole = torch.full((n, 2 * Hq + 2 * Hkv, D), 7.0, device="cuda", dtype=torch.bfloat16)
+    out = whole.split([Hq, Hq, Hkv, Hkv], 1)
+    got = pl.parallax_qk_norm_rope_backward(*(layout(d, L) for d in dy), q, r, k, cs, None, *w,
+                                            seq_len=L, out=out[:3])
+    for a, b in zip(flat, got):
+        assert torch.equal(a, b)
+    assert (out[3] == 7).all()  # the value heads' slice is not touched
+    again = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w)
+    assert all(torch.equal(a, b) for a, b in zip(flat, again))
+    # in place of the incoming gradients
+    d = [x.clone() for x in dy]
+    pl.parallax_qk_norm_rope_backward(*d, q, r, k, cs, pos, *w, out=d)
+    assert all(torch.equal(a, b) for a, b in zip(flat, d))
+
+
+# ------------------------------------------------------------------ append --
+def make_cache(seqs, ps, Hkv, D, dtype, seed, extra=2):
+    """Pools, a table of distinct pages in random order, cu and lens."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-max(n, 1) // ps) for _, n in seqs]
+    pages = sum(need) + extra
+    order = torch.randperm(pages, generator=g).int()
+    table = torch.full((len(seqs), max(need)), -1, dtype=torch.int32)
+    at = 0
+    for b, m in enumerate(need):
+        table[b, :m] = order[at:at + m]
+        at += m
+    pool = lambda s: torch.randn(pages, ps, Hkv, D, generator=torch.Generator().manual_seed(s)).to(dtype)
+    cu = torch.zeros(len(seqs) + 1, dtype=torch.int32)
+    cu[1:] = torch.tensor([q for q, _ in seqs]).cumsum(0)
+    lens = torch.tensor([n for _, n in seqs], dtype=torch.int32)
+    return [x.cuda() for x in (pool(seed), pool(seed + 1), table, cu, lens)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 16, 8), (64, 3, 1)])
+@pytest.mark.parametrize("seqs,ps,pad", [
+    ([(1, 1)], 64, 0), ([(1, 64), (1, 65), (1, 300)], 64, 0),
+    ([(5, 5), (0, 70), (130, 200), (0, 0), (1, 129)], 64, 9),
+    ([(3, 10)] * 70, 16, 1)])
+def test_append(seqs, ps, pad, D, Hq, Hkv, dtype):
+    kp, vp, table, cu, lens = make_cache(seqs, ps, Hkv, D, dtype, seed=40)
+    n = int(cu[-1]) + pad
+    (q, r, k, v), w, _, cs = inputs(n, Hq, Hkv, D, D, dtype, seed=41)
+    want_kp, want_vp = kp.clone(), vp.clone()
+    idx = torch.cat([torch.arange(nn - c, nn) for c, nn in seqs]).cuda()
+    idx = torch.cat([idx, torch.zeros(pad, device="cuda", dtype=idx.dtype)]).int()
+    fq, fr, fk = pl.parallax_qk_norm_rope(q, r, k, cs, idx, *w)  # tested above
+    seq = torch.repeat_interleave(torch.arange(len(seqs)), torch.tensor([c for c, _ in seqs])).cuda()
+    m = n - pad
+    page = table.long()[seq, idx[:m].long() // ps]
+    want_kp[page, idx[:m].long() % ps] = fk[:m]
+    want_vp[page, idx[:m].long() % ps] = v[:m]
+    qo = torch.full((n, Hq, D), 3.0, device="cuda", dtype=dtype)
+    ro = qo.clone()
+    ws = pl.status_workspace("cuda")
+    pl.parallax_norm_rope_append(q, r, k, v, cs, kp, vp, table, lens, cu, None, *w, q_out=qo,
+                                 r_out=ro, workspace=ws)
+    assert torch.equal(kp, want_kp) and torch.equal(vp, want_vp)
+    assert torch.equal(qo[:m], fq[:m]) and torch.equal(ro[:m], fr[:m])
+    assert (qo[m:] == 3).all() and (ro[m:] == 3).all()  # rows past the last sequence
+    assert int(ws[:4].view(torch.int32)) == 0
+    if all(c == 1 for c, _ in seqs):  # one token per sequence: no cu_seqlens needed
+        kp2, vp2, *_ = make_cache(seqs, ps, Hkv, D, dtype, seed=40)
+        q2, r2 = pl.parallax_norm_rope_append(q, r, k, v, cs, kp2, vp2, table, lens, None, None, *w)
+        assert torch.equal(q2, fq) and torch.equal(kp2, want_kp) and torch.equal(vp2, want_vp)
+
+
+def test_append_positions_without_probe_and_bad_slots():
+    seqs, ps, Hq, Hkv, D = [(4, 70), (3, 3), (2, 66)], 64, 4, 2, 64
+    kp, vp, table, cu, lens = make_cache(seqs, ps, Hkv, D, torch.bfloat16, seed=50)
+    (q, _, k, v), w, pos, cs = inputs(9, Hq, Hkv, D, 32, torch.bfloat16, seed=51)
+    want = pl.parallax_qk_norm_rope(q, None, k, cs, pos, w[0], None, w[2], interleaved=True)
+    base_k, base_v = kp.clone(), vp.clone()
+    ws = pl.status_workspace("cuda")
+    run = lambda t, n: pl.parallax_norm_rope_append(q, None, k, v, cs, kp, vp, t, n, cu, pos, w[0],
+                                                    None, w[2], interleaved=True, workspace=ws)
+    qo, ro = run(table, lens)
+    assert ro is None and torch.equal(qo, want[0]) and int(ws[:4].view(torch.int32)) == 0
+    assert torch.equal(kp[table[0, 1], 2:6], want[2][:4]) and torch.equal(vp[table[1, 0], :3], v[4:7])
+    # a page outside the pool, a length that puts keys before 0, one past the table:
+    # those keys are not written, everything else is
+    for t, n in ((table.clone(), lens.clone()), (table, lens.clone()), (table, lens.clone())):
+        kp.copy_(base_k), vp.copy_(base_v), ws.zero_()
+        want_k, want_v = base_k.clone(), base_v.clone()
+        if t is not table:
+            t[2, 1] = kp.shape[0]
+            keep = [(0, range(4)), (1, range(3))]
+        elif keep is not None and len(keep) == 2:
+            n[1] = 1  # tokens 4, 5 before the first key
+            keep = [(0, range(4)), (1, range(2, 3)), (2, range(2))]
+        else:
+            n[0] = 2 ** 31 - 1
+            keep = [(1, range(3)), (2, range(2))]
+        for b, js in keep:
+            for j in js:
+                i = int(n[b]) - seqs[b][0] + j
+                want_k[t[b, i // ps], i % ps] = want[2][int(cu[b]) + j]
+                want_v[t[b, i // ps], i % ps] = v[int(cu[b]) + j]
+        qo, _ = run(t, n)
+        assert torch.equal(kp, want_k) and torch.equal(vp, want_v) and torch.equal(qo, want[0])
+        assert int(ws[:4].view(torch.int32)) == 2
+
+
+def test_streams_graphs_and_devices_context():
+    """On another stream, and captured twice with separate workspaces."""
+    (q, r, k, _), w, pos, cs = inputs(300, 8, 4, 128, 128, torch.bfloat16, seed=60)
+    want = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w)
+    dy = [x.clone() for x in want]
+    wantg = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, stream=s)
+    gotg = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w, stream=s.cuda_stream)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert all(torch.equal(a, b) for a, b in zip(wantg, gotg))
+    graphs = []
+    for _ in range(2):
+        ws = pl.norm_rope_backward_workspace(300, 8, 4, 128, q.device)
+        out = tuple(torch.empty_like(x) for x in want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, out=out, workspace=ws)
+            grads = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w, workspace=ws)
+        graphs.append((graph, out, grads, ws))
+    for graph, *_ in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    for _, out, grads, _ in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(want, out))
+        assert all(torch.equal(a, b) for a, b in zip(wantg, grads))
