@@ -12,11 +12,17 @@
 //   dw = sum over tokens and heads of dz xh              (no weight: dx = dz)
 // All arithmetic is fp32 with one rounding to the output type.
 //
-// Bound: HBM. A row is read once and written once; the table row of a token
-// (4 rot bytes) is read once per warp and kept in registers over the heads.
-// D/16 lanes share a row, 16 values each: two 16-byte chunks for bf16 whose
-// dimensions pair up under the rotation (chunks c and c + rot/16), so the
-// rotation needs no exchange and the norm log2(D/16) shuffles.
+// Bound: HBM for many tokens (a row is read once and written once, the table
+// row of a token, 4 rot bytes, once per warp), launch latency for few.
+//  - D/16 lanes share a row, 16 values each: two chunks of 8 whose dimensions
+//    pair up under the rotation (chunks c and c + rot/16), so the rotation
+//    needs no exchange and the norm log2(D/16) shuffles. A warp holds
+//    32 / (D/16) heads of one token per step.
+//  - A block works on one kind of head (query, probe, key, value), so its
+//    weight stays in registers, multiplied into the token's cosines and sines:
+//    a value costs two packed multiply-adds and a scaling.
+//  - A warp's rows come through a ring of its own in shared memory, a token's
+//    heads by one bulk copy, the next ones in flight while it works.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,23 +33,44 @@
 namespace plx {
 
 constexpr int kNrThreads = 256;
+constexpr int kNrWarps = kNrThreads / 32;
+constexpr unsigned long long kNrTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr unsigned int kNrStatusClamped = 2u;   // PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED
 constexpr unsigned int kNrStatusPosition = 4u;  // PARALLAX_DEVICE_STATUS_POSITION_CLAMPED
+
+// n / d for 0 <= n < 2^31 without a division instruction sequence (Granlund
+// and Montgomery, "Division by invariant integers using multiplication"): with
+// 2^s >= d > 2^(s-1) and m = floor(2^32 (2^s - d) / d) + 1, the quotient is
+// (mulhi(m, n) + n) >> s. Units of work are placed by two divisions each.
+struct NrDivisor {
+  uint32_t d, m, s;
+  __host__ static NrDivisor of(int d) {
+    NrDivisor r{(uint32_t)d, 0, 0};
+    while ((1ull << r.s) < (unsigned long long)d) ++r.s;
+    r.m = (uint32_t)((((1ull << r.s) - d) << 32) / d + 1);
+    return r;
+  }
+  __device__ int quotient(int n) const {
+    return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s);
+  }
+};
 
 struct NormRopeParams {
   // kinds: 0 query, 1 probe, 2 key, 3 value (append only, copied)
   const void* x[4];       // [tokens] rows xs[i] elements apart, heads D apart
-  const void* w[3];       // [D], or nullptr: no norm
-  void* y[3];             // outputs (append: y[2] is unused)
+  const void* w[4];       // [D], or nullptr: no norm
+  void* y[4];             // outputs; append: y[2], y[3] are the pools
   long long xs[4];
   int H[4];               // heads of each kind; 0 leaves it out
   const float* cs;        // [max_pos][rot]: cosines, then sines
   const int32_t* pos;     // [tokens], or nullptr
-  int tokens, rot, interleaved, seq_len, max_pos;
+  int tokens, rot, seq_len, max_pos;
+  NrDivisor seq_div, unit_div[4];  // by seq_len; by a token's units of each kind
   float eps;
   unsigned int* status;
+  int first_block[5];     // blocks of kind i: first_block[i] .. first_block[i + 1]
+  int unit_rows;          // heads of a token that a warp takes at a time
   // append
-  void *k_pages, *v_pages;
   const int32_t *cu, *lens, *table;
   int B, page_size, num_pages, max_pages;
   // backward: dy in the layout of y, dx rows dxs[i] elements apart
@@ -52,19 +79,18 @@ struct NormRopeParams {
   long long dxs[3];
   float* partial;         // [blocks][D] sums of dz xh
   float* dw[3];
-  int first_block[4];     // blocks of kind i: first_block[i] .. first_block[i + 1]
 };
 
 // The two 8-value chunks a lane holds of a D-value row, and which of them the
 // rotation touches. Halves: chunks (i, i + rot/16) rotate as pairs for
 // i < rot/16, the other lanes hold the chunks that pass through. Interleaved:
 // chunks (i, i + D/16), each with its pairs inside.
-template <int D>
+template <int D, bool INTER>
 struct NrLane {
-  int a, b;          // chunk indices
+  int a, b;  // chunk indices
   bool rot_a, rot_b;
-  __device__ NrLane(int i, int rot, int interleaved) {
-    if (interleaved) {
+  __device__ NrLane(int i, int rot) {
+    if (INTER) {
       a = i;
       b = i + D / 16;
       rot_a = a < rot / 8;
@@ -78,101 +104,98 @@ struct NrLane {
   }
 };
 
-template <typename T>
-struct NrChunk;  // 8 values as loaded
-template <>
-struct NrChunk<__nv_bfloat16> {
-  uint4 u;
-  __device__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ void get(float* f) const {
-    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+// 8 values as packed pairs, from or to memory.
+__device__ __forceinline__ void nr_get(const __nv_bfloat16* p, f32x2 (&f)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_lo_to_float(v[i]);
-      f[2 * i + 1] = bf16_hi_to_float(v[i]);
-    }
-  }
-  __device__ void set(const float* f) {
-    u = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                   pack_bf16x2(f[6], f[7]));
-  }
-  __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
-};
-template <>
-struct NrChunk<float> {
-  float4 lo, hi;
-  __device__ void load(const float* p) {
-    lo = reinterpret_cast<const float4*>(p)[0];
-    hi = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ void get(float* f) const {
-    f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w;
-    f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
-  }
-  __device__ void set(const float* f) {
-    lo = make_float4(f[0], f[1], f[2], f[3]);
-    hi = make_float4(f[4], f[5], f[6], f[7]);
-  }
-  __device__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = lo;
-    reinterpret_cast<float4*>(p)[1] = hi;
-  }
-};
-
-// The cosines and sines a lane applies (8 pairs) of one table row.
-template <int D>
-__device__ __forceinline__ void nr_load_angles(const float* row, const NrLane<D>& ln, int rot,
-                                               int interleaved, float (&c)[8], float (&s)[8]) {
-  const float* const sn = row + rot / 2;
-  const auto four = [](const float* p, float* f) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-  };
+  for (int i = 0; i < 4; ++i) f[i] = f2_pack(bf16_lo_to_float(v[i]), bf16_hi_to_float(v[i]));
+}
+__device__ __forceinline__ void nr_get(const float* p, f32x2 (&f)[4]) {
+  const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+  f[0] = f2_pack(u.x, u.y), f[1] = f2_pack(u.z, u.w);
+  f[2] = f2_pack(v.x, v.y), f[3] = f2_pack(v.z, v.w);
+}
+__device__ __forceinline__ void nr_put(__nv_bfloat16* p, const f32x2 (&f)[4]) {
+  uint32_t v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f[i], lo, hi);
+    v[i] = pack_bf16x2(lo, hi);
   }
-  if (interleaved) {
-    if (ln.rot_a) {
-      four(row + 4 * ln.a, c);
-      four(sn + 4 * ln.a, s);
-    }
-    if (ln.rot_b) {
-      four(row + 4 * ln.b, c + 4);
-      four(sn + 4 * ln.b, s + 4);
-    }
-  } else if (ln.rot_a) {
-    four(row + 8 * ln.a, c);
-    four(row + 8 * ln.a + 4, c + 4);
-    four(sn + 8 * ln.a, s);
-    four(sn + 8 * ln.a + 4, s + 4);
-  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void nr_put(float* p, const f32x2 (&f)[4]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(f[i], v[2 * i], v[2 * i + 1]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Rotates v (chunk a in v[0..8), chunk b in v[8..16)) forwards (SIGN = 1) or
-// back (-1). Values outside the rotated dimensions are not touched, so an
-// infinity or a NaN there stays where it is.
-template <int D, int SIGN>
-__device__ __forceinline__ void nr_rotate(float (&v)[16], const NrLane<D>& ln, int interleaved,
-                                          const float (&c)[8], const float (&s)[8]) {
-  const auto turn = [](float& x, float& y, float co, float si) {
-    const float x0 = x, y0 = y, sg = SIGN > 0 ? si : -si;
-    x = x0 * co - y0 * sg;
-    y = x0 * sg + y0 * co;
-  };
-  if (interleaved) {
+// The rotation's factors of one lane: y_a = x_a ca + z_a sa, y_b = x_b cb +
+// z_b sb, where z is the other member of each pair (halves: the other chunk;
+// interleaved: the pair swapped). BACK rotates the other way.
+struct NrAngles {
+  f32x2 ca[4], sa[4], cb[4], sb[4];
+};
+
+template <int D, bool INTER, bool BACK>
+__device__ __forceinline__ NrAngles nr_angles(const float* row, const NrLane<D, INTER>& ln,
+                                              int rot) {
+  NrAngles g;
+  const float* const sn = row + rot / 2;
+  if (INTER) {
+    const auto chunk = [&](int c, bool on, f32x2(&co)[4], f32x2(&si)[4]) {
+      float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (on) {
+        x = *reinterpret_cast<const float4*>(row + 4 * c);
+        y = *reinterpret_cast<const float4*>(sn + 4 * c);
+      }
+      const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        co[i] = f2_pack(xs[i], xs[i]);
+        si[i] = BACK ? f2_pack(ys[i], -ys[i]) : f2_pack(-ys[i], ys[i]);
+      }
+    };
+    chunk(ln.a, ln.rot_a, g.ca, g.sa);
+    chunk(ln.b, ln.rot_b, g.cb, g.sb);
+  } else {
+    const f32x2 minus = f2_pack(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      g.ca[i] = f2_pack(1.f, 1.f);
+      g.sa[i] = 0;
+    }
     if (ln.rot_a) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) turn(v[2 * i], v[2 * i + 1], c[i], s[i]);
+      nr_get(row + 8 * ln.a, g.ca);
+      nr_get(sn + 8 * ln.a, g.sa);
     }
-    if (ln.rot_b) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) turn(v[8 + 2 * i], v[9 + 2 * i], c[4 + i], s[4 + i]);
+    for (int i = 0; i < 4; ++i) {
+      g.cb[i] = g.ca[i];
+      g.sb[i] = BACK ? f2_mul(g.sa[i], minus) : g.sa[i];
+      if (!BACK) g.sa[i] = f2_mul(g.sa[i], minus);
     }
-  } else if (ln.rot_a) {
+  }
+  return g;
+}
+
+// Chunks that the rotation does not touch only take their factor: an infinity
+// or a NaN stays in its place.
+template <int D, bool INTER>
+__device__ __forceinline__ void nr_rotate(f32x2 (&a)[4], f32x2 (&b)[4],
+                                          const NrLane<D, INTER>& ln, const NrAngles& g) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn(v[i], v[8 + i], c[i], s[i]);
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 x = a[i], y = b[i];
+    const f32x2 za = INTER ? f2_swap(x) : y, zb = INTER ? f2_swap(y) : x;
+    a[i] = f2_mul(x, g.ca[i]);
+    b[i] = f2_mul(y, g.cb[i]);
+    if (ln.rot_a) a[i] = f2_fma(za, g.sa[i], a[i]);
+    if (ln.rot_b) b[i] = f2_fma(zb, g.sb[i], b[i]);
   }
 }
 
@@ -184,22 +207,28 @@ __device__ __forceinline__ float nr_row_sum(float x) {
   return x;
 }
 
-template <int D>
-__device__ __forceinline__ float nr_rstd(const float (&v)[16], float eps) {
-  float ss = 0.f;
+// sum of a.x + b.y over a lane's 16 values
+__device__ __forceinline__ float nr_dot(const f32x2 (&a)[4], const f32x2 (&x)[4],
+                                        const f32x2 (&b)[4], const f32x2 (&y)[4]) {
+  f32x2 s = f2_mul(a[0], x[0]), u = f2_mul(b[0], y[0]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
-  return 1.f / sqrtf(nr_row_sum<D>(ss) * (1.f / D) + eps);
+  for (int i = 1; i < 4; ++i) {
+    s = f2_fma(a[i], x[i], s);
+    u = f2_fma(b[i], y[i], u);
+  }
+  float s0, s1, u0, u1;
+  f2_unpack(s, s0, s1);
+  f2_unpack(u, u0, u1);
+  return (s0 + s1) + (u0 + u1);
 }
 
-// Element offset of (token t, head h) in an output: [tokens][H][D], or with
-// seq_len L > 0 [tokens / L][H][L][D].
-__device__ __forceinline__ size_t nr_out_offset(int t, int h, int H, int L, int D) {
-  if (L > 0) return (((size_t)(t / L) * H + h) * L + t % L) * D;
-  return ((size_t)t * H + h) * D;
+// 1 / sqrt(mean(x^2) + eps) of a row
+template <int D>
+__device__ __forceinline__ float nr_rstd(const f32x2 (&a)[4], const f32x2 (&b)[4], float eps) {
+  return rsqrtf(nr_row_sum<D>(nr_dot(a, a, b, b)) * (1.f / D) + eps);
 }
 
-// The table row of token t's position (clamped into the table and flagged).
+// The table row of a position (clamped into the table and flagged).
 __device__ __forceinline__ const float* nr_table_row(const NormRopeParams& p, long long pos) {
   if (pos < 0 || pos >= p.max_pos) {
     atomicOr(p.status, kNrStatusPosition);
@@ -226,221 +255,351 @@ __device__ __forceinline__ int nr_find_sequence(const int32_t* cu, int B, int t)
   return lo;
 }
 
-// Forward. One warp per (token, block of U x 32 / (D/16) head rows); lane
-// group g of the warp takes rows g, g + groups, ... The U loads of a lane are
-// issued before any is used. U = 1 spreads a few tokens over more warps;
-// U = 4 keeps enough bytes in flight for many.
-template <typename T, int D, int U, bool APPEND>
-__global__ void __launch_bounds__(kNrThreads) parallax_norm_rope_kernel(const NormRopeParams p) {
-  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kRows = U * kGroups;
+// The ring of one warp: kStages stages of PARTS x BYTES of head rows, a table
+// row (up to 512 bytes) and a note, filled by bulk copies that an mbarrier per
+// stage counts.
+template <int PARTS, int BYTES, int STAGES>
+struct NrRing {
+  static constexpr int kStages = STAGES, kBytes = BYTES;
+  static constexpr int kStageBytes = PARTS * BYTES + 512 + 16;
+  static constexpr int kWarpBytes = STAGES * (kStageBytes + 16);
+  static constexpr int kSmem = kNrWarps * kWarpBytes;
+  uint8_t* base;  // this warp's
+  __device__ uint8_t* rows(int st, int part) const {
+    return base + st * kStageBytes + part * BYTES;
+  }
+  __device__ float* table(int st) const {
+    return reinterpret_cast<float*>(base + st * kStageBytes + PARTS * BYTES);
+  }
+  __device__ long long* note(int st) const {
+    return reinterpret_cast<long long*>(base + st * kStageBytes + PARTS * BYTES + 512);
+  }
+  __device__ uint32_t bar(int st) const { return smem_u32(base + STAGES * kStageBytes + st * 16); }
+  __device__ void init() const {  // one lane
+    for (int st = 0; st < STAGES; ++st) mbar_init(bar(st), 1);
+    mbar_fence_init();
+  }
+};
+
+// A unit of work is up to `rows` heads of one kind and token. A warp's units
+// are `stride` apart.
+struct NrUnits {
+  int unit, stride, count, rows;
+  NrDivisor per_token;
+  __device__ NrUnits(int first, int stride_, int tokens, const NrDivisor& per, int rows_)
+      : unit(first), stride(stride_), rows(rows_), per_token(per) {
+    count = tokens * (int)per.d;  // below 2^31: the entry points check tokens x heads
+  }
+  __device__ bool valid() const { return unit < count; }
+  __device__ void place(int& t, int& h0) const {
+    t = per_token.quotient(unit);
+    h0 = (unit - t * (int)per_token.d) * rows;
+  }
+  __device__ void next() { unit = unit + stride < unit ? count : unit + stride; }
+};
+
+// 4 KB of rows per stage: 16 heads of 128 bf16 dimensions. Three blocks per SM.
+using NrForwardRing = NrRing<1, 4096, 2>;
+// 2 KB of dy and as much of x. Two blocks per SM.
+using NrBackwardRing = NrRing<2, 2048, 3>;
+
+template <typename T, int D, bool INTER, bool APPEND>
+__global__ void __launch_bounds__(kNrThreads, 3)
+    parallax_norm_rope_kernel(const NormRopeParams p) {
+  using Ring = NrForwardRing;
+  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kSt = Ring::kStages;
+  constexpr int kRowBytes = D * (int)sizeof(T);
+  constexpr int kKinds = APPEND ? 4 : 3;
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % kLanes,
+            grp = lane / kLanes;
+  const Ring ring{ring_bytes + warp * Ring::kWarpBytes};
+  if (lane == 0) ring.init();
+  __syncwarp();
+  int k = 0;
+  while (k < kKinds - 1 && (int)blockIdx.x >= p.first_block[k + 1]) ++k;
+  const int blk = (int)blockIdx.x - p.first_block[k],
+            nblk = p.first_block[k + 1] - p.first_block[k];
+  const int H = p.H[k];
+  const T* const x = static_cast<const T*>(p.x[k]);
+  T* const y = static_cast<T*>(p.y[k]);
+  const T* const wt = static_cast<const T*>(p.w[k]);
+  const long long xs = p.xs[k];
+  const NrLane<D, INTER> ln(li, p.rot);
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, li = lane % kLanes, grp = lane / kLanes;
-  const int heads = p.H[0] + p.H[1] + p.H[2] + (APPEND ? p.H[3] : 0);
-  const int per_token = (heads + kRows - 1) / kRows;
-  const long long unit =
-      (long long)blockIdx.x * (kNrThreads / 32) + (int)(threadIdx.x >> 5);
-  if (unit >= (long long)p.tokens * per_token) return;
-  const int t = (int)(unit / per_token), blk = (int)(unit - (long long)t * per_token);
-  long long pos = t;
-  size_t slot_row = 0;  // append: the token's row of the page pools
-  bool in_cache = false;
-  if (APPEND) {
-    int b = t;
-    long long at;
-    if (p.cu != nullptr) {
-      b = nr_find_sequence(p.cu, p.B, t);
-      if (b < 0) return;  // a padding row: left as it is
-      at = (long long)__ldg(p.lens + b) - __ldg(p.cu + b + 1) + t;
-    } else {
-      at = (long long)__ldg(p.lens + b) - 1;
+  NrUnits at(blk * kNrWarps + warp, nblk * kNrWarps, p.tokens, p.unit_div[k], p.unit_rows),
+      load_at = at;
+  // Starts the copies of the next unit. Its note: the first row (in units of D
+  // elements) of its token's heads in the output, or -1 where it has none.
+  const auto load = [&](int st) {
+    if (!load_at.valid()) return;
+    int t, h0;
+    load_at.place(t, h0);
+    load_at.next();
+    const uint32_t bytes = (uint32_t)(min(load_at.rows, H - h0) * kRowBytes);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(ring.bar(st), bytes + (k < 3 ? p.rot * 4 : 0));
+      bulk_load(smem_u32(ring.rows(st, 0)), x + (size_t)t * xs + (size_t)h0 * D, bytes,
+                ring.bar(st));
     }
-    pos = at;
-    in_cache = at >= 0 && at < (long long)p.max_pages * p.page_size;
-    if (in_cache) {
-      const int page = __ldg(p.table + (size_t)b * p.max_pages + (int)at / p.page_size);
-      in_cache = page >= 0 && page < p.num_pages;
-      slot_row = (size_t)(in_cache ? page : 0) * p.page_size + (int)at % p.page_size;
-    }
-    if (!in_cache && lane == 0) atomicOr(p.status, kNrStatusClamped);
-  } else if (p.seq_len > 0) {
-    pos = t % p.seq_len;
-  }
-  if (p.pos != nullptr) pos = __ldg(p.pos + t);
-  const NrLane<D> ln(li, p.rot, p.interleaved);
-  float c[8], s[8];
-  nr_load_angles<D>(nr_table_row(p, pos), ln, p.rot, p.interleaved, c, s);
-
-  NrChunk<T> xa[U], xb[U];
-  int kind[U], head[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    int h = blk * kRows + u * kGroups + grp;
-    int k = 0;
-    while (k < 4 && h >= p.H[k]) h -= p.H[k++];
-    if (k >= (APPEND ? 4 : 3)) k = -1;
-    kind[u] = k;
-    head[u] = h;
-    if (k >= 0) {
-      const T* const row = static_cast<const T*>(p.x[k]) + (size_t)t * p.xs[k] + (size_t)h * D;
-      xa[u].load(row + 8 * ln.a);
-      xb[u].load(row + 8 * ln.b);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int k = kind[u];
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    if (k >= 0) {
-      xa[u].get(v);
-      xb[u].get(v + 8);
-    }
-    const float rstd = nr_rstd<D>(v, p.eps);  // every lane takes part in the shuffles
-    if (k < 0) continue;
-    T* out;
-    if (APPEND && k >= 2) {
-      if (!in_cache) continue;
-      out = static_cast<T*>(k == 2 ? p.k_pages : p.v_pages) +
-            (slot_row * p.H[k] + (size_t)head[u]) * D;
-    } else {
-      out = static_cast<T*>(p.y[k]) + nr_out_offset(t, head[u], p.H[k], APPEND ? 0 : p.seq_len, D);
-    }
-    if (k < 3) {
-      if (p.w[k] != nullptr) {
-        NrChunk<T> wa, wb;
-        float w[16];
-        wa.load(static_cast<const T*>(p.w[k]) + 8 * ln.a);
-        wb.load(static_cast<const T*>(p.w[k]) + 8 * ln.b);
-        wa.get(w);
-        wb.get(w + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = v[i] * rstd * w[i];
+    long long pos = t, note;
+    if (APPEND) {
+      int b = t;
+      if (p.cu != nullptr) b = nr_find_sequence(p.cu, p.B, t);
+      note = b < 0 ? -1 : (long long)t * H;  // -1: a padding row, left as it is
+      if (b >= 0 && (k >= 2 || p.pos == nullptr)) {
+        pos = (long long)__ldg(p.lens + b) - 1;
+        if (p.cu != nullptr) pos += t + 1 - __ldg(p.cu + b + 1);
+        if (k >= 2) {  // the key's place in the pools
+          note = -1;
+          if (pos >= 0 && pos < (long long)p.max_pages * p.page_size) {
+            const int page = __ldg(p.table + (size_t)b * p.max_pages + (int)pos / p.page_size);
+            if (page >= 0 && page < p.num_pages)
+              note = ((long long)page * p.page_size + (int)pos % p.page_size) * H;
+          }
+          if (note < 0 && lane == 0) atomicOr(p.status, kNrStatusClamped);
+        }
       }
-      nr_rotate<D, 1>(v, ln, p.interleaved, c, s);
-      xa[u].set(v);
-      xb[u].set(v + 8);
+    } else if (p.seq_len > 0) {
+      const int row = p.seq_div.quotient(t), i = t - row * p.seq_len;
+      pos = i;
+      note = (long long)row * H * p.seq_len + i;
+    } else {
+      note = (long long)t * H;
     }
-    xa[u].store(out + 8 * ln.a);
-    xb[u].store(out + 8 * ln.b);
+    if (lane == 0) {
+      if (k < 3) {
+        if (p.pos != nullptr) pos = note >= 0 ? __ldg(p.pos + t) : 0;
+        if (note < 0) pos = max(0LL, min(pos, (long long)p.max_pos - 1));
+        bulk_load(smem_u32(ring.table(st)), nr_table_row(p, pos), p.rot * 4, ring.bar(st));
+      }
+      *ring.note(st) = note;
+    }
+  };
+#pragma unroll 1
+  for (int st = 0; st < kSt; ++st) load(st);
+
+  f32x2 wa[4], wb[4];
+  const bool norm = wt != nullptr;
+  if (norm) {
+    nr_get(wt + 8 * ln.a, wa);
+    nr_get(wt + 8 * ln.b, wb);
+  }
+  // heads of an output row are D apart, or with seq_len > 0 seq_len * D
+  const size_t head_step = (!APPEND && p.seq_len > 0 ? (size_t)p.seq_len : 1) * D;
+  int st = 0;
+  uint32_t parity = 0;
+  for (; at.valid(); at.next()) {
+    int t, h0;
+    at.place(t, h0);
+    if (!mbar_wait_bounded(ring.bar(st), parity, kNrTimeoutNs, nullptr)) {
+      atomicOr(p.status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
+      return;
+    }
+    __syncwarp();  // the note
+    const long long out_row = *ring.note(st);
+    const int n = min(at.rows, H - h0);
+    if (out_row >= 0) {
+      NrAngles ang;
+      if (k < 3) {
+        ang = nr_angles<D, INTER, false>(ring.table(st), ln, p.rot);
+        if (norm) {
+          // the weight belongs to the source of each term: n_a cos, n_b sin, ...
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ang.ca[i] = f2_mul(ang.ca[i], wa[i]);
+            ang.cb[i] = f2_mul(ang.cb[i], wb[i]);
+            ang.sa[i] = f2_mul(ang.sa[i], INTER ? f2_swap(wa[i]) : wb[i]);
+            ang.sb[i] = f2_mul(ang.sb[i], INTER ? f2_swap(wb[i]) : wa[i]);
+          }
+        }
+      }
+      T* out = y + (size_t)out_row * D + (size_t)(h0 + grp) * head_step;
+      const T* row = reinterpret_cast<const T*>(ring.rows(st, 0)) + grp * D;
+#pragma unroll 1
+      for (int h = grp; h < n + grp; h += kGroups) {  // the warp's groups together
+        f32x2 a[4], b[4];
+        nr_get(row + 8 * ln.a, a);  // past the unit's rows: stale, not stored
+        nr_get(row + 8 * ln.b, b);
+        if (k < 3) {
+          const float rstd = norm ? nr_rstd<D>(a, b, p.eps) : 1.f;
+          nr_rotate<D, INTER>(a, b, ln, ang);
+          if (norm) {
+            const f32x2 rr = f2_pack(rstd, rstd);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a[i] = f2_mul(a[i], rr);
+              b[i] = f2_mul(b[i], rr);
+            }
+          }
+        }
+        if (h < n) {
+          nr_put(out + 8 * ln.a, a);
+          nr_put(out + 8 * ln.b, b);
+        }
+        out += kGroups * head_step;
+        row += kGroups * D;
+      }
+    }
+    __syncwarp();  // the warp is done with this stage
+    load(st);
+    if (++st == kSt) {
+      st = 0;
+      parity ^= 1;
+    }
   }
 }
 
-// Backward. The blocks of a kind walk its tokens, one token per warp and
-// step, all its heads (U row blocks at a time); dw stays in 16 registers per
-// lane and is summed over the block's rows in shared memory at the end, one
-// [D] partial per block in a fixed order.
-template <typename T, int D, int U>
+// Backward: dw stays in 16 registers per lane and is summed over the block's
+// rows in shared memory at the end, one [D] partial per block in a fixed order.
+template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kNrThreads, 2)
     parallax_norm_rope_backward_kernel(const NormRopeParams p) {
-  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kWarps = kNrThreads / 32;
-  __shared__ float red[kWarps][D];
-  pdl_wait_primary();
-  pdl_launch_dependents();
+  using Ring = NrBackwardRing;
+  constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kSt = Ring::kStages;
+  constexpr int kRowBytes = D * (int)sizeof(T);
+  extern __shared__ __align__(16) uint8_t ring_bytes[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % kLanes,
             grp = lane / kLanes;
+  const Ring ring{ring_bytes + warp * Ring::kWarpBytes};
+  if (lane == 0) ring.init();
+  __syncwarp();
   int k = 0;
   while (k < 2 && (int)blockIdx.x >= p.first_block[k + 1]) ++k;
-  const int blk = (int)blockIdx.x - p.first_block[k], nblk = p.first_block[k + 1] - p.first_block[k];
+  const int blk = (int)blockIdx.x - p.first_block[k],
+            nblk = p.first_block[k + 1] - p.first_block[k];
   const int H = p.H[k];
   const T* const x = static_cast<const T*>(p.x[k]);
   const T* const dy = static_cast<const T*>(p.dy[k]);
   T* const dx = static_cast<T*>(p.dx[k]);
-  const bool norm = p.w[k] != nullptr;
-  const NrLane<D> ln(li, p.rot, p.interleaved);
-  float w[16], dw[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    w[i] = 1.f;
-    dw[i] = 0.f;
-  }
+  const T* const wt = static_cast<const T*>(p.w[k]);
+  const long long xs = p.xs[k], dxs = p.dxs[k];
+  const bool norm = wt != nullptr;
+  const NrLane<D, INTER> ln(li, p.rot);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  NrUnits at(blk * kNrWarps + warp, nblk * kNrWarps, p.tokens, p.unit_div[k], p.unit_rows),
+      load_at = at;
+  const auto load = [&](int st) {
+    if (!load_at.valid()) return;
+    int t, h0;
+    load_at.place(t, h0);
+    load_at.next();
+    const int n = min(load_at.rows, H - h0);
+    const uint32_t bytes = (uint32_t)(n * kRowBytes);
+    long long pos = t, dy_row = (long long)t * H + h0;
+    if (p.seq_len > 0) {
+      const int row = p.seq_div.quotient(t), i = t - row * p.seq_len;
+      pos = i;
+      dy_row = ((long long)row * H + h0) * p.seq_len + i;
+    }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(ring.bar(st), (norm ? 2 : 1) * bytes + p.rot * 4);
+      if (norm)
+        bulk_load(smem_u32(ring.rows(st, 1)), x + (size_t)t * xs + (size_t)h0 * D, bytes,
+                  ring.bar(st));
+      if (p.pos != nullptr) pos = __ldg(p.pos + t);
+      if (p.seq_len == 0)
+        bulk_load(smem_u32(ring.rows(st, 0)), dy + (size_t)dy_row * D, bytes, ring.bar(st));
+      bulk_load(smem_u32(ring.table(st)), nr_table_row(p, pos), p.rot * 4, ring.bar(st));
+    }
+    if (p.seq_len > 0) {  // a head's rows are seq_len apart: one copy per head
+      __syncwarp();       // after the expected bytes are set
+      if (lane < n)
+        bulk_load(smem_u32(ring.rows(st, 0)) + lane * kRowBytes,
+                  dy + (size_t)(dy_row + (long long)lane * p.seq_len) * D, kRowBytes, ring.bar(st));
+    }
+  };
+#pragma unroll 1
+  for (int st = 0; st < kSt; ++st) load(st);
+
+  f32x2 wa[4], wb[4], da[4] = {0, 0, 0, 0}, db[4] = {0, 0, 0, 0};
   if (norm) {
-    NrChunk<T> wa, wb;
-    wa.load(static_cast<const T*>(p.w[k]) + 8 * ln.a);
-    wb.load(static_cast<const T*>(p.w[k]) + 8 * ln.b);
-    wa.get(w);
-    wb.get(w + 8);
+    nr_get(wt + 8 * ln.a, wa);
+    nr_get(wt + 8 * ln.b, wb);
   }
-  for (long long tt = (long long)blk * kWarps + warp; tt < p.tokens;
-       tt += (long long)nblk * kWarps) {
-    const int t = (int)tt;
-    const long long pos = p.pos != nullptr ? __ldg(p.pos + t) : (p.seq_len > 0 ? t % p.seq_len : t);
-    float c[8], s[8];
-    nr_load_angles<D>(nr_table_row(p, pos), ln, p.rot, p.interleaved, c, s);
-    for (int h0 = 0; h0 < H; h0 += U * kGroups) {
-      NrChunk<T> xa[U], xb[U], ga[U], gb[U];
+  int st = 0;
+  uint32_t parity = 0;
+  for (; at.valid(); at.next()) {
+    int t, h0;
+    at.place(t, h0);
+    if (!mbar_wait_bounded(ring.bar(st), parity, kNrTimeoutNs, nullptr)) {
+      atomicOr(p.status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
+      return;
+    }
+    const int n = min(at.rows, H - h0);
+    const NrAngles ang = nr_angles<D, INTER, true>(ring.table(st), ln, p.rot);
+    T* out = dx + (size_t)t * dxs + (size_t)(h0 + grp) * D;
+    const T* gr = reinterpret_cast<const T*>(ring.rows(st, 0)) + grp * D;
+    const T* xr = reinterpret_cast<const T*>(ring.rows(st, 1)) + grp * D;
+#pragma unroll 1
+    for (int h = grp; h < n + grp; h += kGroups) {  // the warp's groups together
+      f32x2 ga[4], gb[4], a[4], b[4];
+      const bool live = h < n;
+      nr_get(gr + 8 * ln.a, ga);  // past the unit's rows: stale, not stored or summed
+      nr_get(gr + 8 * ln.b, gb);
+      nr_rotate<D, INTER>(ga, gb, ln, ang);  // dz
+      if (norm) {
+        nr_get(xr + 8 * ln.a, a);
+        nr_get(xr + 8 * ln.b, b);
+        const float rstd = nr_rstd<D>(a, b, p.eps);
+        const f32x2 rr = f2_pack(rstd, rstd);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * kGroups + grp;
-        if (h < H) {
-          const T* const g = dy + nr_out_offset(t, h, H, p.seq_len, D);
-          ga[u].load(g + 8 * ln.a);
-          gb[u].load(g + 8 * ln.b);
-          if (norm) {
-            const T* const row = x + (size_t)t * p.xs[k] + (size_t)h * D;
-            xa[u].load(row + 8 * ln.a);
-            xb[u].load(row + 8 * ln.b);
+        for (int i = 0; i < 4; ++i) {
+          a[i] = f2_mul(a[i], rr);  // xh
+          b[i] = f2_mul(b[i], rr);
+          if (live) {
+            da[i] = f2_fma(ga[i], a[i], da[i]);  // dz xh
+            db[i] = f2_fma(gb[i], b[i], db[i]);
           }
+          ga[i] = f2_mul(ga[i], wa[i]);  // dn
+          gb[i] = f2_mul(gb[i], wb[i]);
+        }
+        // rstd (dn - xh mean(dn xh))
+        const float m = nr_row_sum<D>(nr_dot(ga, a, gb, b)) * (-1.f / D);
+        const f32x2 mm = f2_pack(m, m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ga[i] = f2_mul(f2_fma(a[i], mm, ga[i]), rr);
+          gb[i] = f2_mul(f2_fma(b[i], mm, gb[i]), rr);
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * kGroups + grp;
-        float v[16], g[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = g[i] = 0.f;
-        if (h < H) {
-          ga[u].get(g);
-          gb[u].get(g + 8);
-          if (norm) {
-            xa[u].get(v);
-            xb[u].get(v + 8);
-          }
-        }
-        nr_rotate<D, -1>(g, ln, p.interleaved, c, s);
-        if (norm) {
-          const float rstd = nr_rstd<D>(v, p.eps);
-          float dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[i] *= rstd;                    // xh
-            dw[i] = fmaf(g[i], v[i], dw[i]);  // dz xh
-            g[i] *= w[i];                    // dn
-            dot = fmaf(g[i], v[i], dot);
-          }
-          dot = nr_row_sum<D>(dot) * (1.f / D);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) g[i] = rstd * (g[i] - v[i] * dot);
-        }
-        if (h < H) {
-          T* const out = dx + (size_t)t * p.dxs[k] + (size_t)h * D;
-          ga[u].set(g);
-          gb[u].set(g + 8);
-          ga[u].store(out + 8 * ln.a);
-          gb[u].store(out + 8 * ln.b);
-        }
+      if (live) {
+        nr_put(out + 8 * ln.a, ga);
+        nr_put(out + 8 * ln.b, gb);
       }
+      out += kGroups * D;
+      gr += kGroups * D;
+      xr += kGroups * D;
+    }
+    __syncwarp();  // the warp is done with this stage
+    load(st);
+    if (++st == kSt) {
+      st = 0;
+      parity ^= 1;
     }
   }
   if (!norm) return;  // the whole block: one kind
+  __syncthreads();  // every copy has landed; the rings' space now holds the warps' sums
+  float(*const red)[D] = reinterpret_cast<float(*)[D]>(ring_bytes);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    float v[4];
+    f2_unpack(da[i], v[0], v[1]);
+    f2_unpack(db[i], v[2], v[3]);
 #pragma unroll
-    for (int o = kLanes; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-  }
-  if (grp == 0) {
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      red[warp][8 * ln.a + i] = dw[i];
-      red[warp][8 * ln.b + i] = dw[8 + i];
+      for (int o = kLanes; o < 32; o <<= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+      if (grp == 0) red[warp][8 * (j < 2 ? ln.a : ln.b) + 2 * i + (j & 1)] = v[j];
     }
   }
   __syncthreads();
   for (int d = threadIdx.x; d < D; d += kNrThreads) {
     float sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) sum += red[v][d];
+    for (int v = 0; v < kNrWarps; ++v) sum += red[v][d];
     p.partial[(size_t)blockIdx.x * D + d] = sum;
   }
 }

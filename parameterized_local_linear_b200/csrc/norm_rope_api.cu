@@ -1,6 +1,7 @@
 // C ABI of the norm + rotation entry points (include/parallax.h): argument
 // checks and launches of the kernels in kernel_norm_rope.cuh.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "parallax.h"
@@ -26,7 +27,8 @@ bool stride_ok(long long stride, int H, int D, int dtype) {
 int check_common(int tokens, int Hq, int Hkv, int D, int rot, int max_pos, float eps, int dtype,
                  const float* cs, const int32_t* pos, void* ws, size_t ws_bytes, size_t need) {
   if (!cs || !ws) return PARALLAX_ERR_NULL_POINTER;
-  if (tokens < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq > 65535 || max_pos < 1)
+  if (tokens < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq > 65535 || max_pos < 1 ||
+      (long long)tokens * Hq > 0x7fffffffLL)  // (such a tensor does not fit the GPU)
     return PARALLAX_ERR_BAD_SHAPE;
   if (!(eps > 0.f) || !(eps < 3.0e38f)) return PARALLAX_ERR_BAD_SHAPE;
   if (D != 64 && D != 128) return PARALLAX_ERR_UNSUPPORTED_HEAD_DIM;
@@ -46,58 +48,98 @@ int check_rows(const void* x, long long stride, const void* w, int H, int D, int
   return PARALLAX_OK;
 }
 
-template <typename T, int D, int U, bool APPEND>
-int launch_forward(const NormRopeParams& p, cudaStream_t s) {
-  constexpr int kRows = U * 32 / (D / 16);
-  const int heads = p.H[0] + p.H[1] + p.H[2] + (APPEND ? p.H[3] : 0);
-  const long long units = (long long)p.tokens * ((heads + kRows - 1) / kRows);
-  const long long blocks = (units + kNrThreads / 32 - 1) / (kNrThreads / 32);
-  if (blocks > 0x7fffffffLL) return PARALLAX_ERR_BAD_SHAPE;
-  return launch_pdl(parallax_norm_rope_kernel<T, D, U, APPEND>, dim3((unsigned)blocks), kNrThreads,
-                    0, s, p);
+// Blocks of a grid that fits the GPU at once (`most`, a few per SM): each kind
+// as many as its units fill, or where that is more than `most`, its share of
+// the work (one block over would run alone at the end: 445 blocks on 444 places
+// took 100 us where 441 took 73). Many tokens: a unit fills a ring stage
+// (`stage_rows`), so that a token's angles serve all its heads; few (less than
+// two steps of 32 / (D/16) rows per warp): single steps, so that more warps
+// share them. A unit's own part (its copies, angles and place) takes as long as
+// `unit_cost` steps.
+void deal_blocks(NormRopeParams& p, int kinds, int most, int D, int stage_rows, double unit_cost) {
+  const int groups = 32 / (D / 16);
+  long long steps[4] = {}, all_steps = 0, fill[4] = {}, filled = 0;
+  double work[4] = {}, all_work = 0;
+  for (int i = 0; i < kinds; ++i) {
+    steps[i] = (p.H[i] + groups - 1) / groups;
+    all_steps += p.tokens * steps[i];
+  }
+  p.seq_div = NrDivisor::of(std::max(1, p.seq_len));
+  p.unit_rows = all_steps >= 2LL * most * kNrWarps ? stage_rows : groups;
+  for (int i = 0; i < kinds; ++i) {
+    const long long units = (p.H[i] + p.unit_rows - 1) / p.unit_rows;
+    p.unit_div[i] = NrDivisor::of(std::max(1, (int)units));
+    filled += fill[i] = (p.tokens * units + kNrWarps - 1) / kNrWarps;
+    all_work += work[i] = steps[i] + unit_cost * units;
+  }
+  p.first_block[0] = 0;
+  for (int i = 0; i < kinds; ++i) {
+    // kinds that would get no block take one; `most` leaves room for them
+    const long long share = std::max(1LL, (long long)((most - kinds) * work[i] / all_work));
+    p.first_block[i + 1] =
+        p.first_block[i] + (int)(filled <= most ? fill[i] : std::min(share, fill[i]));
+  }
 }
 
-template <typename T, int D, bool APPEND>
-int launch_forward_u(const NormRopeParams& p, cudaStream_t s) {
+constexpr int kNrForwardBlocksPerSm = 3;
+constexpr double kNrForwardUnitCost = 1.5;
+constexpr int kNrBackwardBlocksPerSm = 2;
+
+template <typename T, int D, bool INTER, bool APPEND>
+int launch_forward(NormRopeParams& p, cudaStream_t s) {
+  static std::atomic<int> done[256];
+  auto kernel = parallax_norm_rope_kernel<T, D, INTER, APPEND>;
+  constexpr int kSmem = NrForwardRing::kSmem;
   int sm = 0;
-  const int st = current_sm_count(&sm);
-  if (st != PARALLAX_OK) return st;
-  const int heads = p.H[0] + p.H[1] + p.H[2] + (APPEND ? p.H[3] : 0);
-  constexpr int kRows4 = 4 * 32 / (D / 16);
-  const long long units = (long long)p.tokens * ((heads + kRows4 - 1) / kRows4);
-  return units >= 8LL * sm ? launch_forward<T, D, 4, APPEND>(p, s)
-                           : launch_forward<T, D, 1, APPEND>(p, s);
+  int st = current_sm_count(&sm);
+  if (st != PARALLAX_OK || (st = set_smem_once(kernel, kSmem, done)) != PARALLAX_OK) return st;
+  constexpr int kKinds = APPEND ? 4 : 3;
+  deal_blocks(p, kKinds, kNrForwardBlocksPerSm * sm, D,
+              NrForwardRing::kBytes / (D * (int)sizeof(T)), kNrForwardUnitCost);
+  return launch_pdl(kernel, dim3((unsigned)p.first_block[kKinds]), kNrThreads, kSmem, s, p);
+}
+
+template <bool APPEND, typename T>
+int dispatch_forward_t(NormRopeParams& p, int D, bool inter, cudaStream_t s) {
+  if (D == 128) return inter ? launch_forward<T, 128, true, APPEND>(p, s)
+                             : launch_forward<T, 128, false, APPEND>(p, s);
+  return inter ? launch_forward<T, 64, true, APPEND>(p, s)
+               : launch_forward<T, 64, false, APPEND>(p, s);
 }
 
 template <bool APPEND>
-int dispatch_forward(const NormRopeParams& p, int D, int dtype, cudaStream_t s) {
-  if (dtype == PARALLAX_DTYPE_BF16)
-    return D == 128 ? launch_forward_u<__nv_bfloat16, 128, APPEND>(p, s)
-                    : launch_forward_u<__nv_bfloat16, 64, APPEND>(p, s);
-  return D == 128 ? launch_forward_u<float, 128, APPEND>(p, s)
-                  : launch_forward_u<float, 64, APPEND>(p, s);
+int dispatch_forward(NormRopeParams& p, int D, int inter, int dtype, cudaStream_t s) {
+  return dtype == PARALLAX_DTYPE_BF16
+             ? dispatch_forward_t<APPEND, __nv_bfloat16>(p, D, inter != 0, s)
+             : dispatch_forward_t<APPEND, float>(p, D, inter != 0, s);
 }
 
-// Blocks of the backward kernel: two per SM, dealt to the kinds by their rows,
-// each kind's at most one per 8 tokens.
-constexpr int kNrBackwardBlocksPerSm = 2;
-
-size_t backward_workspace(int sm, int D) {
+size_t backward_workspace(int sm, int D) {  // a partial per block: at most one more per kind
   return kWorkspaceHeaderBytes + (size_t)(kNrBackwardBlocksPerSm * sm + 3) * D * sizeof(float);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool INTER>
 int launch_backward(const NormRopeParams& p, cudaStream_t s) {
-  constexpr int kU = sizeof(T) == 2 ? 2 : 1;  // fp32 rows: 2 at a time spill
-  int st = launch_pdl(parallax_norm_rope_backward_kernel<T, D, kU>, dim3((unsigned)p.first_block[3]),
-                      kNrThreads, 0, s, p);
+  static std::atomic<int> done[256];
+  auto kernel = parallax_norm_rope_backward_kernel<T, D, INTER>;
+  constexpr int kSmem = NrBackwardRing::kSmem;
+  int st = set_smem_once(kernel, kSmem, done);
+  if (st != PARALLAX_OK) return st;
+  st = launch_pdl(kernel, dim3((unsigned)p.first_block[3]), kNrThreads, kSmem, s, p);
   if (st != PARALLAX_OK) return st;
   if (!p.w[0] && !p.w[1] && !p.w[2]) return PARALLAX_OK;
   return launch_pdl(parallax_norm_rope_dw_kernel<D>, dim3(3), 1024, 0, s, p);
 }
 
-NormRopeParams base_params(int tokens, int Hq, int Hkv, int rot, int interleaved, int max_pos,
-                           float eps, const float* cs, const int32_t* pos, bool probe, void* ws) {
+template <typename T>
+int dispatch_backward(const NormRopeParams& p, int D, bool inter, cudaStream_t s) {
+  if (D == 128)
+    return inter ? launch_backward<T, 128, true>(p, s) : launch_backward<T, 128, false>(p, s);
+  return inter ? launch_backward<T, 64, true>(p, s) : launch_backward<T, 64, false>(p, s);
+}
+
+NormRopeParams base_params(int tokens, int Hq, int Hkv, int rot, int max_pos, float eps,
+                           const float* cs, const int32_t* pos, bool probe, void* ws) {
   NormRopeParams p{};
   p.H[0] = Hq;
   p.H[1] = probe ? Hq : 0;
@@ -106,7 +148,6 @@ NormRopeParams base_params(int tokens, int Hq, int Hkv, int rot, int interleaved
   p.pos = pos;
   p.tokens = tokens;
   p.rot = rot;
-  p.interleaved = interleaved != 0;
   p.max_pos = max_pos;
   p.eps = eps;
   p.status = static_cast<unsigned int*>(ws);
@@ -150,14 +191,14 @@ extern "C" int parallax_qk_norm_rope(const void* q, const void* r, const void* k
   if ((st = check_rows(k, k_stride, k_weight, Hkv, D, dtype)) != PARALLAX_OK) return st;
   if (!aligned16(q_out) || !aligned16(k_out) || (probe && !aligned16(r_out)))
     return PARALLAX_ERR_MISALIGNED;
-  NormRopeParams p = base_params(tokens, Hq, Hkv, rotary_dim, interleaved, max_positions, eps,
-                                 cos_sin, positions, probe, workspace);
+  NormRopeParams p = base_params(tokens, Hq, Hkv, rotary_dim, max_positions, eps, cos_sin,
+                                 positions, probe, workspace);
   p.seq_len = seq_len;
   p.x[0] = q, p.x[1] = r, p.x[2] = k;
   p.w[0] = q_weight, p.w[1] = r_weight, p.w[2] = k_weight;
   p.y[0] = q_out, p.y[1] = r_out, p.y[2] = k_out;
   p.xs[0] = q_stride, p.xs[1] = r_stride, p.xs[2] = k_stride;
-  return dispatch_forward<false>(p, D, dtype, static_cast<cudaStream_t>(stream));
+  return dispatch_forward<false>(p, D, interleaved, dtype, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t parallax_qk_norm_rope_backward_workspace_bytes(int tokens, int Hq, int Hkv,
@@ -188,8 +229,8 @@ extern "C" int parallax_qk_norm_rope_backward(
   void* const dx[3] = {dq, dr, dk};
   float* const dw[3] = {dq_weight, dr_weight, dk_weight};
   const long long xs[3] = {q_stride, r_stride, k_stride}, dxs[3] = {dq_stride, dr_stride, dk_stride};
-  NormRopeParams p = base_params(tokens, Hq, Hkv, rotary_dim, interleaved, max_positions, eps,
-                                 cos_sin, positions, probe, workspace);
+  NormRopeParams p = base_params(tokens, Hq, Hkv, rotary_dim, max_positions, eps, cos_sin,
+                                 positions, probe, workspace);
   p.seq_len = seq_len;
   for (int i = 0; i < 3; ++i) {
     if (p.H[i] == 0) continue;
@@ -208,19 +249,12 @@ extern "C" int parallax_qk_norm_rope_backward(
   int sm = 0;
   if ((st = current_sm_count(&sm)) != PARALLAX_OK) return st;
   if (workspace_bytes < backward_workspace(sm, D)) return PARALLAX_ERR_WORKSPACE_TOO_SMALL;
-  const long long rows = (long long)p.H[0] + p.H[1] + p.H[2];
-  for (int i = 0; i < 3; ++i) {
-    const long long share = ((long long)kNrBackwardBlocksPerSm * sm * p.H[i] + rows / 2) / rows;
-    const long long most = ((long long)tokens + kNrThreads / 32 - 1) / (kNrThreads / 32);
-    p.first_block[i + 1] =
-        p.first_block[i] + (p.H[i] == 0 ? 0 : (int)std::max(1LL, std::min(share, most)));
-  }
+  deal_blocks(p, 3, kNrBackwardBlocksPerSm * sm, D,
+              NrBackwardRing::kBytes / (D * (int)elem_size(dtype)), 0.0);
   p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == PARALLAX_DTYPE_BF16)
-    return D == 128 ? launch_backward<__nv_bfloat16, 128>(p, s)
-                    : launch_backward<__nv_bfloat16, 64>(p, s);
-  return D == 128 ? launch_backward<float, 128>(p, s) : launch_backward<float, 64>(p, s);
+  return dtype == PARALLAX_DTYPE_BF16 ? dispatch_backward<__nv_bfloat16>(p, D, interleaved != 0, s)
+                                      : dispatch_backward<float>(p, D, interleaved != 0, s);
 }
 
 extern "C" int parallax_norm_rope_append(
@@ -250,15 +284,13 @@ extern "C" int parallax_norm_rope_append(
       !aligned16(v_pages) || !aligned4(cu_seqlens_q) || !aligned4(cache_seqlens) ||
       !aligned4(block_table))
     return PARALLAX_ERR_MISALIGNED;
-  NormRopeParams p = base_params(total_tokens, Hq, Hkv, rotary_dim, interleaved, max_positions, eps,
-                                 cos_sin, positions, probe, workspace);
+  NormRopeParams p = base_params(total_tokens, Hq, Hkv, rotary_dim, max_positions, eps, cos_sin,
+                                 positions, probe, workspace);
   p.H[3] = Hkv;
   p.x[0] = q, p.x[1] = r, p.x[2] = k, p.x[3] = v;
   p.w[0] = q_weight, p.w[1] = r_weight, p.w[2] = k_weight;
-  p.y[0] = q_out, p.y[1] = r_out;
+  p.y[0] = q_out, p.y[1] = r_out, p.y[2] = k_pages, p.y[3] = v_pages;
   p.xs[0] = q_stride, p.xs[1] = r_stride, p.xs[2] = k_stride, p.xs[3] = v_stride;
-  p.k_pages = k_pages;
-  p.v_pages = v_pages;
   p.cu = cu_seqlens_q;
   p.lens = cache_seqlens;
   p.table = block_table;
@@ -266,5 +298,5 @@ extern "C" int parallax_norm_rope_append(
   p.page_size = page_size;
   p.num_pages = num_pages;
   p.max_pages = max_pages_per_seq;
-  return dispatch_forward<true>(p, D, dtype, static_cast<cudaStream_t>(stream));
+  return dispatch_forward<true>(p, D, interleaved, dtype, static_cast<cudaStream_t>(stream));
 }
