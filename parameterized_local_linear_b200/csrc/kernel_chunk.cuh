@@ -111,12 +111,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
   const uint32_t sQ = base + Geo::kOffQ, sR = base + Geo::kOffR;
   const uint32_t sK = base + Geo::kOffK, sV = base + Geo::kOffV;
   const uint32_t bar = base + Geo::kOffBar;
-  const uint32_t q_full = bar, q_empty = bar + 8, k_full = bar + 16, k_empty = k_full + 8 * kSt,
+  const uint32_t q_full = bar, k_full = bar + 16, k_empty = k_full + 8 * kSt,
                  v_full = k_empty + 8 * kSt, v_ready = v_full + 8 * kSt,
                  v_empty = v_ready + 8 * kSt;
+  // p_full: one per P buffer, since a warp may finish tile j + 1 before another
+  // finishes tile j
   const uint32_t s_full = v_empty + 8 * kSt, s_free = s_full + 8, p_full = s_full + 16,
-                 o_done = s_full + 24, bar_drain = s_full + 32, red_full = s_full + 40;
-  constexpr int kOffMisc = Geo::kOffBar + 16 + 5 * 8 * kSt + 48;
+                 o_done = s_full + 32, bar_drain = s_full + 40, red_full = s_full + 48;
+  constexpr int kOffMisc = Geo::kOffBar + 16 + 5 * 8 * kSt + 64;
   // per stage, one word per 16 keys, written by the warp that converted them:
   // bit 0 the block is fp16, bit 1 the tile's page is in the pool
   int4* const v_info = reinterpret_cast<int4*>(gbase + kOffMisc);
@@ -124,13 +126,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kOffMisc + 20 * kSt);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbase + kOffMisc + 20 * kSt + 4);
   float* const red = reinterpret_cast<float*>(gbase + Geo::kOffRed);
-  static_assert(kOffMisc % 16 == 0 && 16 + 5 * 8 * kSt + 48 + 20 * kSt + 8 <= 512, "misc area");
+  static_assert(kOffMisc % 16 == 0 && 16 + 5 * 8 * kSt + 64 + 20 * kSt + 8 <= 512, "misc area");
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be warp-uniform
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     for (int s = 0; s < kSt; ++s) {
       mbar_init(k_full + 8 * s, 1);
       mbar_init(k_empty + 8 * s, 1);
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     mbar_init(s_full, 1);
     mbar_init(s_free, kPfSoftmaxWarps);
     mbar_init(p_full, kPfSoftmaxWarps);
+    mbar_init(p_full + 8, kPfSoftmaxWarps);
     mbar_init(o_done, 1);
     mbar_init(bar_drain, 1);
     mbar_init(red_full, kPfSoftmaxWarps);
@@ -171,26 +173,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
   const auto round_parity = [](int jt) { return (uint32_t)(jt / kSt) & 1u; };
 
   if (warp == 8) {
-    // ------------------------------------------------------------ producer --
+    // ------------------------------------------------- producer of K and V --
     bool ok = true, skipped_k0 = false;
-    int np = 0, last = -1;  // pieces started, last tile whose K and V loads both started
+    int last = -1;  // the last tile whose K and V loads both started
     int jt = 0;
     while (ok && cur.next(p.sp, pc)) {
-      if (np > 0) ok = mbar_wait_bounded(q_empty, (np - 1) & 1, p.timeout_ns, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        const int tok = pc.s.s0 + pc.rt * p.sp.tpt;
-        const uint32_t rows = (uint32_t)(p.sp.tpt * p.G);
-        mbar_arrive_expect_tx(q_full, (PROBE ? 2 : 1) * Geo::kH * rows * 128u);
-        for (int h = 0; h < Geo::kH; ++h) {
-          tma_load_5d_plain(sQ + h * kChunkRows * 128, &tmQ, 0, 0, tok, h, pc.g, q_full);
-          if (PROBE) tma_load_5d_plain(sR + h * kChunkRows * 128, &tmR, 0, 0, tok, h, pc.g, q_full);
-        }
-      }
-      ++np;
       const int32_t* const row = p.table + (size_t)pc.b * p.max_pages;
       int ids = 0;
       for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
@@ -245,7 +232,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
       // Wait (bounded) until every copy this CTA started has landed: the
       // latest load into each buffer is the last one started there.
-      if (np > 0) mbar_wait_bounded(q_full, (np - 1) & 1, p.timeout_ns, nullptr);
       for (int j = max(0, last - kSt + 1); j <= last; ++j) {
         const int s = j % kSt;
         if (!(j == 0 && skipped_k0))
@@ -260,107 +246,108 @@ __global__ void __launch_bounds__(kChThreads, 1)
     bool ok = true;
     const auto wait_scores = [&](int jt) {  // S, T are free and tile jt's K is here
       const bool got =
-          (jt == 0 || mbar_wait_bounded(s_free, (jt - 1) & 1, p.timeout_ns, abort_flag)) &&
-          mbar_wait_bounded(k_full + 8 * (jt % kSt), round_parity(jt), p.timeout_ns, abort_flag);
+          (jt == 0 || mbar_poll_bounded(s_free, (jt - 1) & 1, p.timeout_ns, abort_flag)) &&
+          mbar_poll_bounded(k_full + 8 * (jt % kSt), round_parity(jt), p.timeout_ns, abort_flag);
       tc_fence_after_sync();
       return __all_sync(0xffffffffu, got) != 0;
     };
     const uint64_t dQ = umma_smem_desc(sQ, 16, 1024), dR = umma_smem_desc(sR, 16, 1024),
                    dK = umma_smem_desc(sK, 16, 1024),
                    dV = umma_smem_desc(sV, kChunkKeys * 128, 1024);  // + bytes / 16
-    const auto scores = [&](int jt) {  // S = Q K^T, T = R K^T
-      const uint64_t k = dK + (uint32_t)((jt % kSt) * (Geo::kKVBytes / 16));
-#pragma unroll
-      for (int x = 0; x < (PROBE ? 2 : 1); ++x) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ko = (kk >> 2) * (kChunkKeys * 128) + (kk & 3) * 32;
-          const uint32_t qo = (kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32;
-          umma_ss_lead(tmem + (x == 0 ? kPfColS : kPfColT), (x == 0 ? dQ : dR) + qo / 16,
-                       k + ko / 16, kIdescS, kk > 0, lead);
-        }
-      }
-      umma_commit_lead(s_full, lead);  // also frees the K stage: softmax warp 0 passes it on
-    };
-    uint32_t fp16 = 0;  // bit kk: keys 16 kk .. +15 of the tile are fp16
-    const auto wait_values = [&](int j) {  // P is written (and V was ready for that)
-      const bool got = mbar_wait_bounded(p_full, j & 1, p.timeout_ns, abort_flag);
-      tc_fence_after_sync();
-      const int4 vi = v_info[j % kSt];
-      fp16 = (vi.x & 1) | (vi.y & 1) << 1 | (vi.z & 1) << 2 | (vi.w & 1) << 3;
-      fp16 = __shfl_sync(0xffffffffu, fp16, 0);
-      return __all_sync(0xffffffffu, got) != 0;
-    };
-    // O_A += P V, O_C += (P o T) V for keys 16 k0 .. 16 k1 - 1 of tile j
-    const auto values = [&](int j, int k0, int k1, uint32_t acc0) {
-      const uint64_t v = dV + (uint32_t)((j % kSt) * (Geo::kKVBytes / 16));
+    // O_A += P V, O_C += (P o T) V for tile jv. fp16: bit kk set where keys
+    // 16 kk .. +15 are; acc0 0: the first product clears O
+    const auto values = [&](int jv, uint32_t fp16, uint32_t acc0) {
+      const uint64_t v = dV + (uint32_t)((jv % kSt) * (Geo::kKVBytes / 16));
       if (fp16 == 15u) {
+        const uint32_t tp = tmem + kPfColP + 64 * (jv & 1);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          if (kk < k0 || kk >= k1) continue;
-          const uint32_t tp = tmem + kPfColP + 64 * (kk >> 1) + 8 * (kk & 1);
-          umma_ts_lead(tmem + Geo::kColOA, tp, v + kk * 128, kIdescPV16, kk > 0 ? 1u : acc0, lead);
+          const uint32_t acc = kk > 0 ? 1u : acc0;
+          umma_ts_lead(tmem + Geo::kColOA, tp + 8 * kk, v + kk * 128, kIdescPV16, acc, lead);
           if (PROBE)
-            umma_ts_lead(tmem + Geo::kColOC, tp + 32, v + kk * 128, kIdescPV16,
-                         kk > 0 ? 1u : acc0, lead);
+            umma_ts_lead(tmem + Geo::kColOC, tp + 32 + 8 * kk, v + kk * 128, kIdescPV16, acc, lead);
         }
       } else {
 #pragma unroll 1
-        for (int kk = k0; kk < k1; ++kk) {
-          const uint32_t tp = tmem + kPfColP + 64 * (kk >> 1) + 8 * (kk & 1);
-          const uint32_t acc = kk > 0 ? 1u : acc0;
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t tp = tmem + kPfColP + 8 * kk, acc = kk > 0 ? 1u : acc0;
           const bool one = (fp16 >> kk & 1u) != 0;
           const uint32_t id = one ? kIdescPV16 : kIdescPV;
           umma_ts_lead(tmem + Geo::kColOA, tp, v + kk * 128, id, acc, lead);
           if (PROBE) umma_ts_lead(tmem + Geo::kColOC, tp + 32, v + kk * 128, id, acc, lead);
           if (!one) {
-            umma_ts_lead(tmem + Geo::kColOA, tp + 16, v + kk * 128, id, 1u, lead);
-            if (PROBE) umma_ts_lead(tmem + Geo::kColOC, tp + 48, v + kk * 128, id, 1u, lead);
+            umma_ts_lead(tmem + Geo::kColOA, tp + 64, v + kk * 128, id, 1u, lead);
+            if (PROBE) umma_ts_lead(tmem + Geo::kColOC, tp + 96, v + kk * 128, id, 1u, lead);
           }
         }
       }
     };
-    // Per tile: its scores, then the value products of the tile before. The
-    // waits for the next tile's scores fall between those products, so that
-    // the tensor pipe has work queued while they are checked.
-    int jt = 0, np = 0;
-    uint32_t acc0 = 0;  // 0: tile jt - 1 was the first of its piece and clears O
-    while (ok && cur.next(p.sp, pc)) {
-      bool waited = false;
-      for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
-        const bool start = j == pc.t0;
-        if (start) {
-          if (jt > 0) {
-            // the last tile of the piece before, ahead of the wait for the new Q and R
-            if (!(ok = wait_values(jt - 1))) break;
-            values(jt - 1, 0, 4, acc0);
-            umma_commit_lead(o_done, lead);
-          }
-          const bool got = mbar_wait_bounded(q_full, np++ & 1, p.timeout_ns, abort_flag);
-          if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
+    int np = 0;  // pieces whose Q and R loads started
+    const auto load_queries = [&](const ChunkPiece& x) {
+      if (lead) {
+        const int tok = x.s.s0 + x.rt * p.sp.tpt;
+        mbar_arrive_expect_tx(q_full, (PROBE ? 2 : 1) * Geo::kH * (uint32_t)(p.sp.tpt * p.G) * 128u);
+        for (int h = 0; h < Geo::kH; ++h) {
+          tma_load_5d_plain(sQ + h * kChunkRows * 128, &tmQ, 0, 0, tok, h, x.g, q_full);
+          if (PROBE) tma_load_5d_plain(sR + h * kChunkRows * 128, &tmR, 0, 0, tok, h, x.g, q_full);
         }
-        if (!waited && !(ok = wait_scores(jt))) break;
-        scores(jt);
-        waited = false;
-        if (!start) {
-          if (!(ok = wait_values(jt - 1))) break;
-          values(jt - 1, 0, 3, acc0);
-          if (j + 1 < pc.t1 && !(ok = waited = wait_scores(jt + 1))) break;
-          values(jt - 1, 3, 4, acc0);
-          umma_commit_lead(o_done, lead);  // also frees the V stage: softmax warp 0 passes it on
-        }
-        acc0 = start ? 0u : 1u;
       }
-    }
-    if (ok && jt > 0 && (ok = wait_values(jt - 1))) {
-      values(jt - 1, 0, 4, acc0);
-      umma_commit_lead(o_done, lead);
+      __syncwarp();
+      ++np;
+    };
+    // Per tile: its scores, then the value products of the tile before. The next
+    // piece's Q and R load as soon as the last scores are done.
+    int jt = 0;
+    bool more = cur.next(p.sp, pc);
+    if (more) load_queries(pc);
+    while (ok && more) {
+      ChunkPiece nx;
+      more = cur.next(p.sp, nx);
+      const bool got = mbar_wait_bounded(q_full, (np - 1) & 1, p.timeout_ns, abort_flag);
+      if (!(ok = __all_sync(0xffffffffu, got) != 0)) break;
+      for (int j = pc.t0; j <= pc.t1; ++j) {
+        if (j < pc.t1) {  // S = Q K^T, T = R K^T
+          if (!(ok = wait_scores(jt))) break;
+          const uint64_t k = dK + (uint32_t)((jt % kSt) * (Geo::kKVBytes / 16));
+#pragma unroll
+          for (int x = 0; x < (PROBE ? 2 : 1); ++x) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t ko = (kk >> 2) * (kChunkKeys * 128) + (kk & 3) * 32;
+              const uint32_t qo = (kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32;
+              umma_ss_lead(tmem + (x == 0 ? kPfColS : kPfColT), (x == 0 ? dQ : dR) + qo / 16,
+                           k + ko / 16, kIdescS, kk > 0, lead);
+            }
+          }
+          umma_commit_lead(s_full, lead);  // also frees the K stage: softmax warp 0 passes it on
+          ++jt;
+        } else if (more) {
+          const bool done = mbar_wait_bounded(s_full, (jt - 1) & 1, p.timeout_ns, abort_flag);
+          if (!(ok = __all_sync(0xffffffffu, done) != 0)) break;
+          load_queries(nx);
+        }
+        if (j > pc.t0) {  // tile jv: P is written (and V was ready for that)
+          const int jv = j < pc.t1 ? jt - 2 : jt - 1;
+          const bool full = mbar_poll_bounded(p_full + 8 * (jv & 1), (uint32_t)(jv >> 1) & 1u,
+                                              p.timeout_ns, abort_flag);
+          if (!(ok = __all_sync(0xffffffffu, full) != 0)) break;
+          tc_fence_after_sync();
+          const int4 vi = v_info[jv % kSt];
+          const uint32_t fp16 = __shfl_sync(
+              0xffffffffu, (vi.x & 1) | (vi.y & 1) << 1 | (vi.z & 1) << 2 | (vi.w & 1) << 3, 0);
+          values(jv, fp16, j > pc.t0 + 1 ? 1u : 0u);
+          umma_commit_lead(o_done, lead);
+        }
+      }
+      pc = nx;
     }
     if (!ok && lead) {
       *abort_flag = 1;
       atomicOr(p.status, 1u);
     }
-    umma_commit_lead(bar_drain, lead);  // every UMMA issued above is done once this arrives
+    // the last Q and R loads have landed, and every UMMA issued above is done
+    if (np > 0) mbar_wait_bounded(q_full, (np - 1) & 1, p.timeout_ns, nullptr);
+    umma_commit_lead(bar_drain, lead);
     mbar_wait_bounded(bar_drain, 0, p.timeout_ns, nullptr);
   } else if (warp >= 10) {
     // ------------------------------- V: bf16 to fp16, rows past the end to 0 --
@@ -375,42 +362,61 @@ __global__ void __launch_bounds__(kChThreads, 1)
           ok = false;
           break;
         }
-#pragma unroll 1
-        for (int w = warp - 10; w < kChunkKeys / 16; w += kChConvertWarps) {  // keys 16 w .. +15
-          const int held = pc.s.n - j * kChunkKeys - 16 * w;  // this block's rows below the length
-          uint4* const blk =
-              reinterpret_cast<uint4*>(gbase + Geo::kOffV + st * Geo::kKVBytes) + w * 16 * 8 + lane;
-          uint4 x[kWords];
-          uint32_t mx = 0;
+        // both of this warp's blocks of 16 keys at once: warp - 10 and the next but one
+        constexpr int kBlocks = kChunkKeys / 16 / kChConvertWarps;
+        uint4* const tile = reinterpret_cast<uint4*>(gbase + Geo::kOffV + st * Geo::kKVBytes) + lane;
+        const int left = pc.s.n - j * kChunkKeys;  // rows of the tile below the length
+        // word i of block y: row (i % 4) * 4 + lane / 8 (8 words in each half)
+        const auto word = [&](int y, int i) -> uint4& {
+          const int w = warp - 10 + kChConvertWarps * y;
+          return tile[(i / 4) * kChunkKeys * 8 + w * 16 * 8 + (i % 4) * 32];
+        };
+        uint4 x[kBlocks][kWords];
 #pragma unroll
-          for (int i = 0; i < kWords; ++i) {  // a row is 8 words in each 64-dimension half
-            const int half = i / 4, off = (i % 4) * 32;
-            x[i] = blk[half * kChunkKeys * 8 + off];
-            if ((off + lane) / 8 >= held) x[i] = make_uint4(0, 0, 0, 0);
-            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int y = 0; y < kBlocks; ++y)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mx = __vmaxu2(mx, u[y] & 0x7fff7fffu);
+          for (int i = 0; i < kWords; ++i) x[y][i] = word(y, i);
+        if (left < kChunkKeys) {
+#pragma unroll
+          for (int y = 0; y < kBlocks; ++y)
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+              if ((warp - 10 + kChConvertWarps * y) * 16 + (i % 4) * 4 + lane / 8 >= left)
+                x[y][i] = make_uint4(0, 0, 0, 0);
+        }
+        bool f16[kBlocks];
+#pragma unroll
+        for (int y = 0; y < kBlocks; ++y) {
+          uint32_t mx[4] = {0, 0, 0, 0};  // independent chains
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) {
+            mx[0] = max_abs_bf16x2(mx[0], x[y][i].x);
+            mx[1] = max_abs_bf16x2(mx[1], x[y][i].y);
+            mx[2] = max_abs_bf16x2(mx[2], x[y][i].z);
+            mx[3] = max_abs_bf16x2(mx[3], x[y][i].w);
           }
-          mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-          // bf16 bits: 2^16 is 0x4780, 2^-8 is 0x3b80
-          const bool f16 = mx == 0 || (mx >= 0x3b80u && mx < 0x4780u);
-          if (f16 || held < 16) {
+          mx[0] = max_abs_bf16x2(max_abs_bf16x2(mx[0], mx[1]), max_abs_bf16x2(mx[2], mx[3]));
+          mx[0] &= 0x7fff7fffu;
+          const uint32_t m = __reduce_max_sync(0xffffffffu, max(mx[0] & 0xffffu, mx[0] >> 16));
+          // bf16 bits: 2^16 is 0x4780, 2^-8 is 0x3b80; a NaN is one in fp16 too
+          f16[y] = m == 0 || (m >= 0x3b80u && m < 0x4780u);
+          if (f16[y]) {
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
-              const int half = i / 4, off = (i % 4) * 32;
-              if (f16) {
-                x[i].x = pack_f16x2(bf16_lo_to_float(x[i].x), bf16_hi_to_float(x[i].x));
-                x[i].y = pack_f16x2(bf16_lo_to_float(x[i].y), bf16_hi_to_float(x[i].y));
-                x[i].z = pack_f16x2(bf16_lo_to_float(x[i].z), bf16_hi_to_float(x[i].z));
-                x[i].w = pack_f16x2(bf16_lo_to_float(x[i].w), bf16_hi_to_float(x[i].w));
-              }
-              blk[half * kChunkKeys * 8 + off] = x[i];
+              uint4& v = x[y][i];
+              v.x = pack_f16x2(bf16_lo_to_float(v.x), bf16_hi_to_float(v.x));
+              v.y = pack_f16x2(bf16_lo_to_float(v.y), bf16_hi_to_float(v.y));
+              v.z = pack_f16x2(bf16_lo_to_float(v.z), bf16_hi_to_float(v.z));
+              v.w = pack_f16x2(bf16_lo_to_float(v.w), bf16_hi_to_float(v.w));
             }
-            fence_proxy_async_smem();  // the UMMAs read these rows through the async proxy
           }
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) word(y, i) = x[y][i];
           if (lane == 0)
-            reinterpret_cast<int*>(v_info + st)[w] = (f16 ? 1 : 0) | (tile_ok[st] ? 2 : 0);
+            reinterpret_cast<int*>(v_info + st)[warp - 10 + kChConvertWarps * y] =
+                (f16[y] ? 1 : 0) | (tile_ok[st] ? 2 : 0);
         }
+        fence_proxy_async_smem();  // the UMMAs read these rows through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(v_ready + 8 * st);
       }
@@ -420,181 +426,204 @@ __global__ void __launch_bounds__(kChThreads, 1)
       atomicOr(p.status, 1u);
     }
   } else {
-    // ------------------------------------- softmax: two threads per row --
+    // ------------------------------------------------------------ softmax --
+    // Warp w has 16 rows of its quarter of the TMEM lanes: four threads share
+    // rows ra and ra + 8 (tmem_ld16x64), each with 16 of the 64 keys.
     const int quarter = warp & 3, half = warp >> 2;
-    const int r = quarter * 32 + lane;
-    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_base + kPfColS, tT = tmem + lane_base + kPfColT;
-    const uint32_t tP = tmem + lane_base + kPfColP + 64 * half;  // this half's 64 columns
+    const int ra = quarter * 32 + half * 16 + (lane >> 2), col = 2 * (lane & 3);
+    const uint32_t t16 = tmem + ((uint32_t)(quarter * 32 + half * 16) << 16);
     const float c = p.scale_log2;
-    const int r_tok = r / p.G, r_head = r - r_tok * p.G;
+    const int tok_a = ra / p.G, tok_b = (ra + 8) / p.G;
+    // the epilogue's row: one per thread and half of the columns
+    const int r = quarter * 32 + lane, r_tok = r / p.G, r_head = r - r_tok * p.G;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    struct Row {
+      float m, l, b;                // running max, sums over this thread's keys
+      float s_scale, s_unscale;     // 2^sigma, 2^-sigma; the first tile sets them
+    };
     bool ok = true;
     int jt = 0, np = 0;
-    while (ok && cur.next(p.sp, pc)) {
+    int freed = 0;         // tiles whose V stage is passed back
+    bool wide = false;     // the tile before filled both P buffers
+    bool more = cur.next(p.sp, pc);
+    while (ok && more) {
+      ChunkPiece nx;
+      more = cur.next(p.sp, nx);
       const int j0 = pc.rt * p.sp.tpt;
       const int ntok = min(p.sp.tpt, pc.s.q - j0);  // tokens of this row tile
-      const bool live = r_tok < ntok;
-      // keys below klim are seen by this row, keys below kall by every row
+      // keys below lim are seen by a row, keys below kall by every row
       const int seen0 = p.sp.causal ? pc.s.n - pc.s.q + j0 + 1 : pc.s.n;  // the first token's
-      const int klim = live ? (p.sp.causal ? min(pc.s.n, seen0 + r_tok) : pc.s.n) : 0;
-      const int kall = min(pc.s.n, seen0);
-      float m_used = kNegInf, l = 0.f, bsum = 0.f;
-      // 2^sigma and 2^-sigma; the first tile that is worked on sets them
-      float s_scale = 0.f, s_unscale = 0.f;
+      const auto row_limit = [&](int tok) {
+        if (tok >= ntok) return 0;
+        return p.sp.causal ? min(pc.s.n, seen0 + tok) : pc.s.n;
+      };
+      const int lim_a = row_limit(tok_a), lim_b = row_limit(tok_b), kall = min(pc.s.n, seen0);
+      Row A{kNegInf, 0.f, 0.f, 0.f, 0.f}, B = A;
       for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
         const int st = jt % kSt;
-        ok = mbar_wait_bounded(s_full, jt & 1, p.timeout_ns, abort_flag);
+        // the tile's V is ready, and its flags with it, before its scores are
+        ok = mbar_wait_bounded(v_ready + 8 * st, round_parity(jt), p.timeout_ns, abort_flag);
+        const int4 vi = v_info[st];
+        const bool in_pool = (vi.x & 2) != 0;
+        const bool f16 = (vi.x & vi.y & vi.z & vi.w & 1) != 0;
+        ok = ok && mbar_wait_bounded(s_full, jt & 1, p.timeout_ns, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        // S_j, T_j complete: the score UMMAs have read K_j (and Q, R at a piece's end)
+        float sv[32], tv[32];
+        tmem_ld16x64(t16 + kPfColS, sv);
+        if constexpr (PROBE) tmem_ld16x64(t16 + kPfColT, tv);
+        // S_j, T_j complete: the score UMMAs have read K_j, and the value UMMAs
+        // of tile j - 2, issued before them, V and P of that tile
         if (warp == 0 && lane == 0) {
           mbar_arrive(k_empty + 8 * st);
-          if (j == pc.t1 - 1) mbar_arrive(q_empty);
+          for (; freed < jt - 1; ++freed) mbar_arrive(v_empty + 8 * (freed % kSt));
         }
-        // The other half's scores are only needed for the row's largest t and |s|
-        float sv[32], tv[32];
-        tmem_ld32(tS + 32 * (half ^ 1), sv);
-        if constexpr (PROBE) tmem_ld32(tT + 32 * (half ^ 1), tv);
-        ok = mbar_wait_bounded(v_ready + 8 * st, round_parity(jt), p.timeout_ns, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          tmem_wait_ld();
-          break;
-        }
-        const int4 vi = v_info[st];
-        const bool in_pool = (vi.x & 2) != 0;
-        const bool f16 = (vi.x & vi.y & vi.z & vi.w & 1) != 0;
-        const int k0 = j * kChunkKeys;
-        const bool whole = in_pool && k0 + kChunkKeys <= kall;  // nothing to mask
-        const int lim = in_pool ? klim : 0;
-        float mx = kNegInf, my = kNegInf, sx = 0.f, sy = 0.f;
-        const auto reduce = [&](int kfirst, bool keep) {
-          if (whole) {
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {  // two chains
-              mx = max3(mx, sv[x], sv[x + 1]);
-              my = max3(my, sv[x + 2], sv[x + 3]);
-              if constexpr (PROBE) {
-                sx = max3_abs(sx, tv[x], tv[x + 1]);
-                sy = max3_abs(sy, tv[x + 2], tv[x + 3]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const bool own = kfirst + x < lim;
-              const float sm = own ? sv[x] : kNegInf;
-              mx = fmaxf(mx, sm);
-              if (keep) sv[x] = sm;
-              if constexpr (PROBE) {
-                const float tm = own ? tv[x] : 0.f;
-                sx = fmaxf(sx, fabsf(tm));
-                if (keep) tv[x] = tm;
-              }
-            }
-          }
-        };
-        tmem_wait_ld();
-        reduce(k0 + 32 * (half ^ 1), false);
-        tmem_ld32(tS + 32 * half, sv);
-        if constexpr (PROBE) tmem_ld32(tT + 32 * half, tv);
         tmem_wait_ld();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
-        reduce(k0 + 32 * half, true);
-        sx = fmaxf(sx, sy);
-        mx = fmaxf(mx, my) * c;  // the scale is positive: this is the max of the scaled scores
-        // lazy rescale: keep the stale max unless this tile exceeds it by 2^4,
-        // and 2^sigma unless |s| 2^sigma reaches 2^11
-        float alpha = 1.f, alpha_s = 1.f;
-        const bool grow_m = mx > m_used + 4.f;
-        const bool grow_s = PROBE && !(sx * s_scale < 2048.f && s_scale > 0.f);
-        if (grow_m) {
-          alpha = m_used == kNegInf ? 0.f : ex2_approx(m_used - mx);
-          m_used = mx;
+        // mask
+        const int k0 = j * kChunkKeys;
+        if (!(in_pool && k0 + kChunkKeys <= kall)) {
+          const int la = in_pool ? lim_a - k0 - col : 0, lb = in_pool ? lim_b - k0 - col : 0;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const bool own = 8 * (x >> 2) + (x & 1) < ((x & 2) ? lb : la);
+            sv[x] = own ? sv[x] : kNegInf;
+            if constexpr (PROBE) tv[x] = own ? tv[x] : 0.f;
+          }
         }
-        if (grow_s) {
-          // sx 2^sigma in [2^8, 2^9): room to grow before the next change
-          const int ex = max((int)((__float_as_uint(sx) >> 23) & 0xffu) - 127, -100);
-          const float ns = __int_as_float((135 - ex) << 23);
-          alpha_s = ns * s_unscale;
-          s_scale = ns;
-          s_unscale = __int_as_float((119 + ex) << 23);
+        // Lazy rescale: keep the stale max unless this tile exceeds it by 2^4,
+        // and 2^sigma unless |s| 2^sigma reaches 2^11.
+        const auto within = [&](const Row& w, float mx, float sx) {
+          return mx * c <= w.m + 4.f && (!PROBE || (sx * w.s_scale < 2048.f && w.s_scale > 0.f));
+        };
+        float alpha[2] = {1.f, 1.f}, alpha_c[2] = {1.f, 1.f};  // factors of l, A and of b, C
+        const auto update = [&](float ma, float mb, float sa, float sb) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            Row& w = y ? B : A;
+            float mx = (y ? mb : ma) * c, sx = y ? sb : sa;  // (the scale is positive)
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              sx = fmaxf(sx, __shfl_xor_sync(0xffffffffu, sx, o));
+            }
+            float alpha_s = 1.f;
+            if (mx > w.m + 4.f) {
+              alpha[y] = w.m == kNegInf ? 0.f : ex2_approx(w.m - mx);
+              w.m = mx;
+            }
+            if (PROBE && !(sx * w.s_scale < 2048.f && w.s_scale > 0.f)) {
+              // sx 2^sigma in [2^8, 2^9): room to grow before the next change
+              const int ex = max((int)((__float_as_uint(sx) >> 23) & 0xffu) - 127, -100);
+              const float ns = __int_as_float((135 - ex) << 23);
+              alpha_s = ns * w.s_unscale;
+              w.s_scale = ns;
+              w.s_unscale = __int_as_float((119 + ex) << 23);
+            }
+            alpha_c[y] = alpha[y] * alpha_s;
+            w.l *= alpha[y];
+            w.b *= alpha_c[y];
+          }
+        };
+        const f32x2 c2 = f2_pack(c, c);
+        f32x2 lt[2], bt[2];  // per row: the sums of the even and the odd keys
+        f32x2 nm[2], ss[2];
+        const auto factors = [&]() {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const Row& w = y ? B : A;
+            const float neg_m = (w.m == kNegInf ? 0.f : -w.m) + 11.f;  // no key yet: e = 0
+            nm[y] = f2_pack(neg_m, neg_m);
+            const float sc = w.s_scale * (1.f / 2048.f);  // of e 2^11
+            ss[y] = f2_pack(sc, sc);
+            lt[y] = bt[y] = 0;
+          }
+        };
+        // fp16 weights of the 32 values
+        uint32_t ph[16], th[PROBE ? 16 : 1];
+        const auto weights = [&]() {
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {  // pair u / 2 of row u % 2
+            const int y = u & 1;
+            float e0, e1;
+            ch_exp2(f2_pack(sv[2 * u], sv[2 * u + 1]), c2, nm[y], e0, e1);
+            ph[u] = pack_f16x2(e0, e1);
+            const f32x2 a = f2_pack(f16_lo_to_float(ph[u]), f16_hi_to_float(ph[u]));
+            lt[y] = f2_add(lt[y], a);
+            if constexpr (PROBE) {  // e s from the rounded e: the weights P applies
+              float x0, x1;
+              f2_unpack(f2_mul(f2_mul(a, ss[y]), f2_pack(tv[2 * u], tv[2 * u + 1])), x0, x1);
+              th[u] = pack_f16x2(x0, x1);
+              bt[y] = f2_add(bt[y], f2_pack(f16_lo_to_float(th[u]), f16_hi_to_float(th[u])));
+            }
+          }
+        };
+        float ma = sv[0], mb = sv[2], sa = 0.f, sb = 0.f;  // the largest t and |s| of both rows
+#pragma unroll
+        for (int x = 0; x < 32; x += 4) {
+          ma = max3(ma, sv[x], sv[x + 1]);
+          mb = max3(mb, sv[x + 2], sv[x + 3]);
+          if constexpr (PROBE) {
+            sa = max3_abs(sa, tv[x], tv[x + 1]);
+            sb = max3_abs(sb, tv[x + 2], tv[x + 3]);
+          }
         }
-        const bool grow = grow_m || grow_s;
-        const float alpha_c = alpha * alpha_s;
-        const float neg_m = (m_used == kNegInf ? 0.f : -m_used) + 11.f;  // no key yet: e = 0
-        const f32x2 c2 = f2_pack(c, c), nm2 = f2_pack(neg_m, neg_m);
-        const float ss = s_scale * (1.f / 2048.f);  // of e 2^11
-        const f32x2 ss2 = f2_pack(ss, ss);
-        f32x2 lt = 0, bt = 0;  // (+0, +0)
-        // P is single-buffered and O may need a rescale: the value products of
-        // the tile before must be done
+        const bool grow =
+            __any_sync(0xffffffffu, !(within(A, ma, sa) && within(B, mb, sb)) && in_pool);
+        if (grow) update(ma, mb, sa, sb);  // (the row's four threads need a common value)
+        factors();
+        if (f16) weights();
+        // A tile of fp16 blocks alternates between two P buffers, and its buffer
+        // is free (above). One with hi + lo weights fills both. O may need a
+        // rescale. For either, the products of the tile before must be done.
         const auto prev_done_and_rescale = [&]() -> bool {
-          if (j == pc.t0) return true;
+          const bool wait = j > pc.t0 && (grow || wide || !f16);
+          wide = !f16;
+          if (!wait) return true;
           const bool got = mbar_wait_bounded(o_done, (jt - 1) & 1, p.timeout_ns, abort_flag);
           if (!__all_sync(0xffffffffu, got)) return false;
           tc_fence_after_sync();
-          if (warp == 0 && lane == 0) mbar_arrive(v_empty + 8 * ((jt - 1) % kSt));
-          if (__any_sync(0xffffffffu, grow) && (PROBE || half == 0)) {  // warp-uniform
-            const uint32_t tO = tmem + lane_base + (half ? Geo::kColOC : Geo::kColOA);
-            const float f = half ? alpha_c : alpha;  // 1 on the rows that keep theirs
+          if (grow) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
+            for (int c0 = 0; c0 < (PROBE ? 2 * D : D); c0 += 64) {
+              const float fa = c0 < D ? alpha[0] : alpha_c[0], fb = c0 < D ? alpha[1] : alpha_c[1];
               float o[32];
-              tmem_ld32(tO + c0, o);
+              tmem_ld16x64(t16 + Geo::kColOA + c0, o);  // O_C follows O_A
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] *= f;
-              tmem_st32(tO + c0, o);
+              for (int x = 0; x < 32; ++x) o[x] *= (x & 2) ? fb : fa;
+              tmem_st16x64(t16 + Geo::kColOA + c0, o);
             }
           }
           return true;
         };
         if (f16) {
-          uint32_t ph[16], th[PROBE ? 16 : 1];
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            float e0, e1;
-            ch_exp2(f2_pack(sv[2 * u], sv[2 * u + 1]), c2, nm2, e0, e1);
-            ph[u] = pack_f16x2(e0, e1);
-            const f32x2 a = f2_pack(f16_lo_to_float(ph[u]), f16_hi_to_float(ph[u]));
-            lt = f2_add(lt, a);
-            if constexpr (PROBE) {  // e s from the rounded e: the weights P applies
-              float x0, x1;
-              f2_unpack(f2_mul(f2_mul(a, ss2), f2_pack(tv[2 * u], tv[2 * u + 1])), x0, x1);
-              th[u] = pack_f16x2(x0, x1);
-              bt = f2_add(bt, f2_pack(f16_lo_to_float(th[u]), f16_hi_to_float(th[u])));
-            }
-          }
           if (!prev_done_and_rescale()) {
             ok = false;
             break;
           }
-          tmem_st16u(tP, ph);
-          if constexpr (PROBE) tmem_st16u(tP + 32, th);
+          tmem_st16x32u(t16 + kPfColP + 64 * (jt & 1), ph);
+          if constexpr (PROBE) tmem_st16x32u(t16 + kPfColP + 64 * (jt & 1) + 32, th);
         } else {
           if (!prev_done_and_rescale()) {
             ok = false;
             break;
           }
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {  // 16 keys: fp16, or bf16 hi + lo
-            const bool g16 = ((half ? (g ? vi.w : vi.z) : (g ? vi.y : vi.x)) & 1) != 0;
-            uint32_t hi[8], lo[8], thi[8], tlo[8];
+          for (int g = 0; g < 4; ++g) {  // 16 keys: fp16, or bf16 hi + lo
+            const bool g16 = ((g == 0 ? vi.x : g == 1 ? vi.y : g == 2 ? vi.z : vi.w) & 1) != 0;
+            uint32_t hi[4], lo[4], thi[4], tlo[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < 4; ++u) {
+              const int y = u & 1, x = 8 * g + 2 * u;
               float e0, e1, t0 = 0.f, t1 = 0.f;
-              const int x = 16 * g + 2 * u;
-              ch_exp2(f2_pack(sv[x], sv[x + 1]), c2, nm2, e0, e1);
-              if constexpr (PROBE) {
-                t0 = tv[x] * ss;
-                t1 = tv[x + 1] * ss;
-              }
+              ch_exp2(f2_pack(sv[x], sv[x + 1]), c2, nm[y], e0, e1);
+              if constexpr (PROBE) f2_unpack(f2_mul(ss[y], f2_pack(tv[x], tv[x + 1])), t0, t1);
               lo[u] = tlo[u] = 0;
               if (g16) {
                 hi[u] = pack_f16x2(e0, e1);
@@ -611,35 +640,53 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 t1 = round17(e1 * t1);
                 split_hi_lo(t0, t1, thi[u], tlo[u]);
               }
-              lt = f2_add(lt, f2_pack(e0, e1));
-              bt = f2_add(bt, f2_pack(t0, t1));
+              lt[y] = f2_add(lt[y], f2_pack(e0, e1));
+              bt[y] = f2_add(bt[y], f2_pack(t0, t1));
             }
-            tmem_st8u(tP + 8 * g, hi);
-            tmem_st8u(tP + 16 + 8 * g, lo);
+            tmem_st16x8u(t16 + kPfColP + 8 * g, hi);
+            tmem_st16x8u(t16 + kPfColP + 64 + 8 * g, lo);
             if constexpr (PROBE) {
-              tmem_st8u(tP + 32 + 8 * g, thi);
-              tmem_st8u(tP + 48 + 8 * g, tlo);
+              tmem_st16x8u(t16 + kPfColP + 32 + 8 * g, thi);
+              tmem_st16x8u(t16 + kPfColP + 96 + 8 * g, tlo);
             }
           }
-        }
-        float x0, x1;  // the sums of the even and of the odd keys
-        f2_unpack(lt, x0, x1);
-        l = l * alpha + (x0 + x1);
-        if constexpr (PROBE) {
-          f2_unpack(bt, x0, x1);
-          bsum = bsum * alpha_c + (x0 + x1);
         }
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(p_full + 8 * (jt & 1));
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          Row& w = y ? B : A;
+          float x0, x1;
+          f2_unpack(lt[y], x0, x1);
+          w.l += x0 + x1;
+          if constexpr (PROBE) {
+            f2_unpack(bt[y], x0, x1);
+            w.b += x0 + x1;
+          }
+        }
       }
       if (!ok) break;
-      // l and b of the two key halves meet in shared memory (two buffers: a
-      // warp that writes the next piece's may run ahead of this one's readers)
+      // The rows' sums over their four threads, and what else the epilogue's
+      // threads need, through shared memory (two buffers: a warp that writes
+      // the next piece's may run ahead of this one's readers)
       float* const rd = red + (np & 1) * 4 * kChunkRows;
-      rd[half * kChunkRows + r] = l;
-      if constexpr (PROBE) rd[(2 + half) * kChunkRows + r] = bsum;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        Row& w = y ? B : A;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          w.l += __shfl_xor_sync(0xffffffffu, w.l, o);
+          w.b += __shfl_xor_sync(0xffffffffu, w.b, o);
+        }
+        if ((lane & 3) == 0) {
+          rd[ra + 8 * y] = w.l;
+          rd[kChunkRows + ra + 8 * y] = w.b;
+          rd[2 * kChunkRows + ra + 8 * y] = w.s_unscale;
+          rd[3 * kChunkRows + ra + 8 * y] = w.m;
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(red_full);
       ok = mbar_wait_bounded(red_full, np & 1, p.timeout_ns, abort_flag) &&
@@ -649,20 +696,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
         break;
       }
       ++np;
-      const float lsum = rd[r] + rd[kChunkRows + r];
-      const float bfull =
-          PROBE ? (rd[2 * kChunkRows + r] + rd[3 * kChunkRows + r]) * s_unscale * 2048.f : 0.f;
       tc_fence_after_sync();
-      if (warp == 0 && lane == 0) mbar_arrive(v_empty + 8 * ((jt - 1) % kSt));
+      if (warp == 0 && lane == 0)
+        for (; freed < jt; ++freed) mbar_arrive(v_empty + 8 * (freed % kSt));
+      const bool live = r_tok < ntok;
+      const float lsum = rd[r], cs = rd[2 * kChunkRows + r] * 2048.f;
       // l and A carry 2^11; C and b, which carry 2^sigma, are brought to it
+      const float bfull = PROBE ? rd[kChunkRows + r] * cs : 0.f;
       const float inv = lsum > 0.f ? 1.f / lsum : 0.f, bl = bfull * inv;
-      const float cs = s_unscale * 2048.f;
       const size_t orow =
           ((size_t)(pc.s.s0 + j0 + r_tok) * p.Hq + (size_t)pc.g * p.G + r_head) * D;
       float* const rec =
           p.records + (size_t)piece_slot((int)blockIdx.x, pc.first) * chunk_rec_floats(D);
       if (!pc.complete && live && half == 0) {
-        rec[r] = m_used;
+        rec[r] = rd[3 * kChunkRows + r];
         rec[kChunkRows + r] = lsum;
         rec[2 * kChunkRows + r] = bfull;
       }
@@ -702,6 +749,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         __syncwarp();
       }
       tc_fence_before_sync();  // O is read: the next piece's products follow p_full
+      pc = nx;
     }
     if (!ok) {
       *abort_flag = 1;
