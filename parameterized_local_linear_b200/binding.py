@@ -9,7 +9,6 @@ no CUDA device is present, the calls raise.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -495,104 +494,39 @@ def parallax_prefill(q, r, k, v, scale: Optional[float] = None, causal: bool = T
 
 
 # ------------------------------------- norm and rotation of the heads, chunks --
+# These calls check and pass their tensors in csrc/marshal.cpp.
 
-def _in_context(fn):
-    """Runs a binding function on its first tensor's device and, with stream=,
-    inside that stream, so that what the call allocates belongs to it."""
-
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError(f"{fn.__name__}: expected CUDA tensors")
-        if stream is None and first.device.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
-        with torch.cuda.device(first.device):
-            if stream is None:
-                return fn(first, *args, **kw)
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=first.device)
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
-
-    return call
+def _marshal():
+    global _marshal_module
+    if _marshal_module is None:
+        load_library()
+        path = _build.MARSHAL
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m parameterized_local_linear_b200.build`")
+        from . import _marshal as m
+        _marshal_module = m
+    return _marshal_module
 
 
-def _entry(name, spec):
-    """The C entry point with its argument types set once (p pointer, i int,
-    f float, d double, l long long, z size_t)."""
-    fn = getattr(load_library(), name)
-    if fn.argtypes is None:
-        types = {"p": ctypes.c_void_p, "i": ctypes.c_int, "f": ctypes.c_float,
-                 "d": ctypes.c_double, "l": ctypes.c_longlong, "z": ctypes.c_size_t}
-        fn.argtypes = [types[c] for c in spec]
-        fn.restype = ctypes.c_int
-    return fn
+_marshal_module = None
 
 
-def _head_rows(name, t, like, heads=None):
-    """Token rows [tokens, H, D] whose heads are contiguous; their token stride.
-    `like`: a tensor whose token count, D, dtype and device they share."""
-    if t.dim() != 3 or t.device != like.device or t.dtype != like.dtype:
-        raise ValueError(f"{name} must be [tokens, H, D] with q's dtype and device")
-    n, H, D = t.shape
-    if n != like.shape[0] or D != like.shape[2] or (heads is not None and H != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, which does not match q's "
-                         f"{tuple(like.shape)}")
-    s = t.stride()
-    if s[2] != 1 or (H > 1 and s[1] != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if n > 1 else max(s[0], H * D)
+def _call(name, args, stream):
+    """The marshalled call on the first tensor's device; with stream=, inside
+    that stream, so that what the call allocates belongs to it."""
+    fn = getattr(_marshal_module or _marshal(), name)
+    if stream is None:
+        return fn(*args)
+    device = args[0].device
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
-def _weight_ptr(name, w, like):
-    if w is None:
-        return None
-    if (w.shape != (like.shape[2],) or w.dtype != like.dtype or w.device != like.device
-            or not w.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous [D] tensor with q's dtype and device")
-    return w.data_ptr()
-
-
-def _dense(name, t, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}")
-    return t
-
-
-def _int32(name, t, shape, device):
-    if t is None:
-        return None
-    return _dense(name, t, shape, torch.int32, device).data_ptr()
-
-
-def _buffer(workspace, device, make):
-    buf = make(device) if workspace is None else (
-        workspace.buffer if isinstance(workspace, Workspace) else workspace)
-    if buf.device != device or buf.dtype != torch.uint8 or not buf.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return buf
-
-
-def _rope_inputs(q, r, k, cos_sin, positions):
-    """The checks the norm and rotation calls share: (q, r, k strides, rotary_dim)."""
-    if q.dtype not in _DTYPE_CODE:
-        raise ValueError("q, r, k must be bf16 or fp32")
-    sq = _head_rows("q", q, q)
-    sr = 0 if r is None else _head_rows("r", r, q, q.shape[1])
-    sk = _head_rows("k", k, q)
-    if (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous()
-            or cos_sin.device != q.device):
-        raise ValueError("cos_sin must be a contiguous fp32 [max_positions, rotary_dim] tensor "
-                         "on q's device")
-    return sq, sr, sk, _int32("positions", positions, (q.shape[0],), q.device)
-
-
-def _out_shape(tokens, heads, D, seq_len):
-    if seq_len == 0:
-        return (tokens, heads, D)
-    if seq_len < 0 or tokens % seq_len != 0:
-        raise ValueError("tokens must be a multiple of seq_len")
-    return (tokens // seq_len, heads, seq_len, D)
+def _workspace_buffer(workspace):
+    return workspace.buffer if isinstance(workspace, Workspace) else workspace
 
 
 def status_workspace(device):
@@ -600,34 +534,50 @@ def status_workspace(device):
     return torch.zeros(256, dtype=torch.uint8, device=device)
 
 
-def _header_zeroed(nbytes, device):
-    if nbytes == 0:
-        raise RuntimeError("invalid arguments for a workspace size")
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+def _sized_workspace(name, args, device):
+    fn = getattr(load_library(), name)
+    fn.argtypes = [ctypes.c_int] * len(args)
+    fn.restype = ctypes.c_size_t
+    with torch.cuda.device(device):
+        nbytes = int(fn(*args))
+        if nbytes == 0:
+            raise RuntimeError(f"{name}: invalid arguments")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:256].zero_()
     return ws
+
+
+def norm_rope_backward_workspace(tokens: int, Hq: int, Hkv: int, D: int, device):
+    """A workspace for parallax_qk_norm_rope_backward on `device`."""
+    return _sized_workspace("parallax_qk_norm_rope_backward_workspace_bytes",
+                            (tokens, Hq, Hkv, D), device)
+
+
+def prefill_paged_workspace(B: int, total_tokens: int, Hq: int, Hkv: int, D: int, device):
+    """A workspace for parallax_prefill_paged on `device`."""
+    return _sized_workspace("parallax_prefill_paged_workspace_bytes",
+                            (B, total_tokens, Hq, Hkv, D), device)
 
 
 def parallax_rope_table(max_positions: int, rotary_dim: int, base: float = 1e6, device="cuda",
                         stream=None):
     """The cosines and sines of positions 0 .. max_positions - 1, fp32
     [max_positions, rotary_dim] (rotary_dim / 2 cosines, then the sines)."""
+    fn = load_library().parallax_rope_table
+    fn.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_double, ctypes.c_void_p]
+    fn.restype = ctypes.c_int
     out = torch.empty(max_positions, rotary_dim, dtype=torch.float32, device=device)
-    return _rope_table_into(out, float(base), stream=stream)
-
-
-@_in_context
-def _rope_table_into(out, base):
-    fn = _entry("parallax_rope_table", "piidp")
-    _check(fn(out.data_ptr(), out.shape[0], out.shape[1], base, _stream(None)),
-           "parallax_rope_table")
+    with torch.cuda.device(out.device):
+        if stream is not None:
+            out.record_stream(stream)
+        _check(fn(out.data_ptr(), max_positions, rotary_dim, float(base), _stream(stream)),
+               "parallax_rope_table")
     return out
 
 
-@_in_context
 def parallax_qk_norm_rope(q, r, k, cos_sin, positions=None, q_weight=None, r_weight=None,
                           k_weight=None, eps: float = 1e-6, interleaved: bool = False,
-                          seq_len: int = 0, out=None, workspace=None):
+                          seq_len: int = 0, out=None, workspace=None, stream=None):
     """Per-head RMS norm and rotation of the query, probe and key heads.
 
     q [tokens, Hq, D], r like q or None, k [tokens, Hkv, D] (bf16 or fp32; token
@@ -635,171 +585,51 @@ def parallax_qk_norm_rope(q, r, k, cos_sin, positions=None, q_weight=None, r_wei
     cos_sin as parallax_rope_table gives it, positions int32 [tokens] or None
     (0, 1, ... in each row of seq_len tokens). Returns (q, r, k), contiguous
     [tokens, H, D], or with seq_len = L [tokens / L, H, L, D]; out: three
-    tensors to write (a q that is contiguous may be its own output). Also takes
-    stream=."""
-    sq, sr, sk, pos = _rope_inputs(q, r, k, cos_sin, positions)
-    (n, Hq, D), Hkv = q.shape, k.shape[1]
-    shape_q, shape_k = _out_shape(n, Hq, D, seq_len), _out_shape(n, Hkv, D, seq_len)
-    new = lambda shape: torch.empty(shape, dtype=q.dtype, device=q.device)
-    if out is None:
-        qo, ro, ko = new(shape_q), None if r is None else new(shape_q), new(shape_k)
-    else:
-        qo, ro, ko = out
-        _dense("out[0]", qo, shape_q, q.dtype, q.device)
-        _dense("out[2]", ko, shape_k, q.dtype, q.device)
-        if r is not None:
-            _dense("out[1]", ro, shape_q, q.dtype, q.device)
-    buf = _buffer(workspace, q.device, status_workspace)
-    fn = _entry("parallax_qk_norm_rope", "ppppppppppp" "iiiiiiif" "lll" "ii" "ppz")
-    rc = fn(q.data_ptr(), _ptr(r), k.data_ptr(), _weight_ptr("q_weight", q_weight, q),
-            _weight_ptr("r_weight", r_weight, q), _weight_ptr("k_weight", k_weight, q),
-            cos_sin.data_ptr(), pos, qo.data_ptr(), _ptr(ro) if r is not None else None,
-            ko.data_ptr(), n, Hq, Hkv, D, cos_sin.shape[1], int(bool(interleaved)),
-            cos_sin.shape[0], eps, sq, sr, sk, seq_len, _DTYPE_CODE[q.dtype], _stream(None),
-            buf.data_ptr(), buf.numel())
-    _check(rc, "parallax_qk_norm_rope")
-    return qo, ro if r is not None else None, ko
+    tensors to write (a q that is contiguous may be its own output)."""
+    return _call("qk_norm_rope",
+                 (q, r, k, cos_sin, positions, q_weight, r_weight, k_weight, eps, interleaved,
+                  seq_len, out, _workspace_buffer(workspace)), stream)
 
 
-def norm_rope_backward_workspace(tokens: int, Hq: int, Hkv: int, D: int, device):
-    """A workspace for parallax_qk_norm_rope_backward on `device`."""
-    fn = load_library().parallax_qk_norm_rope_backward_workspace_bytes
-    fn.argtypes = [ctypes.c_int] * 4
-    fn.restype = ctypes.c_size_t
-    with torch.cuda.device(device):
-        return _header_zeroed(int(fn(tokens, Hq, Hkv, D)), device)
-
-
-@_in_context
 def parallax_qk_norm_rope_backward(dq_out, dr_out, dk_out, q, r, k, cos_sin, positions=None,
                                    q_weight=None, r_weight=None, k_weight=None,
                                    eps: float = 1e-6, interleaved: bool = False,
-                                   seq_len: int = 0, out=None, workspace=None):
+                                   seq_len: int = 0, out=None, workspace=None, stream=None):
     """The gradients of parallax_qk_norm_rope: (dq, dr, dk, dq_weight,
     dr_weight, dk_weight) from the gradients of its outputs (in their layout)
     and its inputs. The rows' gradients are [tokens, H, D] in q's dtype (out:
     three tensors to write, token rows as free as q's), the weights' fp32 [D],
-    None where the weight or r is None. Also takes stream=."""
-    sq, sr, sk, pos = _rope_inputs(q, r, k, cos_sin, positions)
-    (n, Hq, D), Hkv = q.shape, k.shape[1]
-    shape_q, shape_k = _out_shape(n, Hq, D, seq_len), _out_shape(n, Hkv, D, seq_len)
-    _dense("dq_out", dq_out, shape_q, q.dtype, q.device)
-    _dense("dk_out", dk_out, shape_k, q.dtype, q.device)
-    if r is not None:
-        _dense("dr_out", dr_out, shape_q, q.dtype, q.device)
-    if out is None:
-        new = lambda H: torch.empty((n, H, D), dtype=q.dtype, device=q.device)
-        dq, dr, dk = new(Hq), None if r is None else new(Hq), new(Hkv)
-    else:
-        dq, dr, dk = out
-    tq = _head_rows("out[0]", dq, q, Hq)
-    tr = 0 if r is None else _head_rows("out[1]", dr, q, Hq)
-    tk = _head_rows("out[2]", dk, q, Hkv)
-    grad = lambda w: None if w is None else torch.empty(D, dtype=torch.float32, device=q.device)
-    dqw, drw, dkw = grad(q_weight), grad(r_weight if r is not None else None), grad(k_weight)
-    buf = _buffer(workspace, q.device, lambda dev: norm_rope_backward_workspace(n, Hq, Hkv, D, dev))
-    fn = _entry("parallax_qk_norm_rope_backward",
-                "ppppppppppp" "pppppp" "iiiiiiif" "llllll" "ii" "ppz")
-    rc = fn(dq_out.data_ptr(), _ptr(dr_out) if r is not None else None, dk_out.data_ptr(),
-            q.data_ptr(), _ptr(r), k.data_ptr(), _weight_ptr("q_weight", q_weight, q),
-            _weight_ptr("r_weight", r_weight, q), _weight_ptr("k_weight", k_weight, q),
-            cos_sin.data_ptr(), pos, dq.data_ptr(), _ptr(dr) if r is not None else None,
-            dk.data_ptr(), _ptr(dqw), _ptr(drw), _ptr(dkw), n, Hq, Hkv, D, cos_sin.shape[1],
-            int(bool(interleaved)), cos_sin.shape[0], eps, sq, sr, sk, tq, tr, tk, seq_len,
-            _DTYPE_CODE[q.dtype], _stream(None), buf.data_ptr(), buf.numel())
-    _check(rc, "parallax_qk_norm_rope_backward")
-    return dq, dr if r is not None else None, dk, dqw, drw, dkw
+    None where the weight or r is None."""
+    return _call("qk_norm_rope_backward",
+                 (dq_out, dr_out, dk_out, q, r, k, cos_sin, positions, q_weight, r_weight, k_weight,
+                  eps, interleaved, seq_len, out, _workspace_buffer(workspace)), stream)
 
 
-def _pool(k_pages, v_pages, block_table, B, Hkv, D, dtype, device):
-    if k_pages.dim() != 4 or k_pages.shape[2:] != (Hkv, D):
-        raise ValueError("k_pages must be [num_pages, page_size, Hkv, D]")
-    _dense("k_pages", k_pages, k_pages.shape, dtype, device)
-    _dense("v_pages", v_pages, k_pages.shape, dtype, device)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages_per_seq]")
-    return _int32("block_table", block_table, block_table.shape, device)
-
-
-@_in_context
 def parallax_norm_rope_append(q, r, k, v, cos_sin, k_pages, v_pages, block_table, cache_seqlens,
                               cu_seqlens_q=None, positions=None, q_weight=None, r_weight=None,
                               k_weight=None, eps: float = 1e-6, interleaved: bool = False,
-                              q_out=None, r_out=None, workspace=None):
+                              q_out=None, r_out=None, workspace=None, stream=None):
     """parallax_qk_norm_rope for the new tokens of sequences with a paged cache:
     returns (q, r) normed and rotated; k (likewise) and v go into the pools.
 
     cache_seqlens int32 [B]: the lengths after the append. cu_seqlens_q int32
     [B + 1]: each sequence's rows, or None for one token per sequence; rows
     past the last are left alone. positions int32 [tokens] or None (each
-    token's key index). Also takes stream=."""
-    sq, sr, sk, pos = _rope_inputs(q, r, k, cos_sin, positions)
-    (n, Hq, D), Hkv = q.shape, k.shape[1]
-    sv = _head_rows("v", v, q, Hkv)
-    B = cache_seqlens.shape[0]
-    table = _pool(k_pages, v_pages, block_table, B, Hkv, D, q.dtype, q.device)
-    lens = _int32("cache_seqlens", cache_seqlens, (B,), q.device)
-    cu = _int32("cu_seqlens_q", cu_seqlens_q, (B + 1,), q.device)
-    if q_out is None:
-        q_out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
-    if r_out is None and r is not None:
-        r_out = torch.empty((n, Hq, D), dtype=q.dtype, device=q.device)
-    _dense("q_out", q_out, (n, Hq, D), q.dtype, q.device)
-    if r is not None:
-        _dense("r_out", r_out, (n, Hq, D), q.dtype, q.device)
-    buf = _buffer(workspace, q.device, status_workspace)
-    fn = _entry("parallax_norm_rope_append", "ppppppppp" "ppp" "pppp" "iiiiiiiif" "llll" "iiii" "ppz")
-    rc = fn(q.data_ptr(), _ptr(r), k.data_ptr(), v.data_ptr(),
-            _weight_ptr("q_weight", q_weight, q), _weight_ptr("r_weight", r_weight, q),
-            _weight_ptr("k_weight", k_weight, q), cos_sin.data_ptr(), pos, cu, lens, table,
-            q_out.data_ptr(), _ptr(r_out) if r is not None else None, k_pages.data_ptr(),
-            v_pages.data_ptr(), B, n, Hq, Hkv, D, cos_sin.shape[1], int(bool(interleaved)),
-            cos_sin.shape[0], eps, sq, sr, sk, sv, k_pages.shape[0], k_pages.shape[1],
-            block_table.shape[1], _DTYPE_CODE[q.dtype], _stream(None), buf.data_ptr(),
-            buf.numel())
-    _check(rc, "parallax_norm_rope_append")
-    return q_out, r_out if r is not None else None
+    token's key index)."""
+    return _call("norm_rope_append",
+                 (q, r, k, v, cos_sin, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q,
+                  positions, q_weight, r_weight, k_weight, eps, interleaved, q_out, r_out,
+                  _workspace_buffer(workspace)), stream)
 
 
-def prefill_paged_workspace(B: int, total_tokens: int, Hq: int, Hkv: int, D: int, device):
-    """A workspace for parallax_prefill_paged on `device`."""
-    fn = load_library().parallax_prefill_paged_workspace_bytes
-    fn.argtypes = [ctypes.c_int] * 5
-    fn.restype = ctypes.c_size_t
-    with torch.cuda.device(device):
-        return _header_zeroed(int(fn(B, total_tokens, Hq, Hkv, D)), device)
-
-
-@_in_context
 def parallax_prefill_paged(q, r, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q=None,
                            scale: Optional[float] = None, causal: bool = True, probe: bool = True,
-                           out=None, workspace=None):
+                           out=None, workspace=None, stream=None):
     """Attention of new tokens over the paged cache that already holds them:
     q, r [tokens, Hq, D] bf16, sequence b's rows cu_seqlens_q[b]:cu_seqlens_q[b+1]
     (None: one token per sequence), the last of its cache_seqlens[b] keys.
     causal: row j of c sees keys up to its own. Rows past the last sequence are
-    left as they are (zero when this call makes the output). Also takes stream=."""
-    if q.dim() != 3 or q.dtype != torch.bfloat16:
-        raise ValueError("q must be [tokens, Hq, D] bf16")
-    n, Hq, D = q.shape
-    _dense("q", q, q.shape, torch.bfloat16, q.device)
-    if probe:
-        if r is None:
-            raise ValueError("r must be a contiguous bf16 tensor shaped like q")
-        _dense("r", r, q.shape, torch.bfloat16, q.device)
-    B, Hkv = cache_seqlens.shape[0], k_pages.shape[2]
-    table = _pool(k_pages, v_pages, block_table, B, Hkv, D, torch.bfloat16, q.device)
-    lens = _int32("cache_seqlens", cache_seqlens, (B,), q.device)
-    cu = _int32("cu_seqlens_q", cu_seqlens_q, (B + 1,), q.device)
-    if out is None:
-        out = torch.zeros_like(q) if cu is not None else torch.empty_like(q)
-    _dense("out", out, q.shape, torch.bfloat16, q.device)
-    buf = _buffer(workspace, q.device, lambda dev: prefill_paged_workspace(B, n, Hq, Hkv, D, dev))
-    fn = _entry("parallax_prefill_paged", "pppppppp" "iiiiifip" "iiii" "pz")
-    rc = fn(q.data_ptr(), _ptr(r) if probe else None, k_pages.data_ptr(), v_pages.data_ptr(),
-            table, cu, lens, out.data_ptr(), B, n, Hq, Hkv, D,
-            D ** -0.5 if scale is None else float(scale), int(bool(causal)), _stream(None),
-            k_pages.shape[0], k_pages.shape[1], block_table.shape[1], int(bool(probe)),
-            buf.data_ptr(), buf.numel())
-    _check(rc, "parallax_prefill_paged")
-    return out
+    left as they are (zero when this call makes the output)."""
+    return _call("prefill_paged",
+                 (q, r, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q, scale, causal,
+                  probe, out, _workspace_buffer(workspace)), stream)
