@@ -36,8 +36,10 @@ int encode_rows_by_group(CUtensorMap* map, const void* base, int D, int total, i
   return r == CUDA_SUCCESS ? PARALLAX_OK : PARALLAX_ERR_CUDA;
 }
 
+// The status header, what to merge per CTA, and two partial records per CTA.
+size_t chunk_records_offset(int ctas) { return kWorkspaceHeaderBytes + ctas * sizeof(ChunkMerge); }
 size_t chunk_workspace(int ctas, int D) {
-  return kWorkspaceHeaderBytes + (size_t)2 * ctas * chunk_rec_floats(D) * sizeof(float);
+  return chunk_records_offset(ctas) + (size_t)2 * ctas * chunk_rec_floats(D) * sizeof(float);
 }
 
 template <int D, bool PROBE>
@@ -106,7 +108,8 @@ int run_chunk(const void* q, const void* r, const void* k_pages, const void* v_p
                     Hkv,          kChunkRows / p.G, causal != 0};
   p.out = static_cast<__nv_bfloat16*>(out);
   p.status = static_cast<unsigned int*>(workspace);
-  p.records = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
+  p.merges = reinterpret_cast<ChunkMerge*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
+  p.records = reinterpret_cast<float*>(static_cast<char*>(workspace) + chunk_records_offset(sm));
   p.table = block_table;
   p.Hq = Hq;
   p.page_size = page_size;

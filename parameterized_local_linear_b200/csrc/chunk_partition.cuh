@@ -34,6 +34,7 @@ struct ChunkSpace {
 
 struct ChunkSeq {
   int s0, q, n;  // first packed row, new tokens, cached keys
+  int nrt;       // row tiles
 };
 
 __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
@@ -41,6 +42,7 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
   s.s0 = min(max(__ldg(sp.cu + b), 0), sp.total);
   s.q = min(max(__ldg(sp.cu + b + 1), s.s0), sp.total) - s.s0;
   s.n = clamp_len(__ldg(sp.lens + b), sp.Lmax);
+  s.nrt = (s.q + sp.tpt - 1) / sp.tpt;
   return s;
 }
 
@@ -51,23 +53,40 @@ __device__ __forceinline__ bool chunk_seq_clamped(const ChunkSpace& sp, int b) {
   return a < 0 || e < a || e > sp.total || n < 0 || n > sp.Lmax || (sp.causal && n < e - a);
 }
 
-// Keys the last row of row tile rt sees, and the tiles that hold them.
-__device__ __forceinline__ int chunk_kend(const ChunkSpace& sp, const ChunkSeq& s, int rt) {
-  if (!sp.causal) return s.n;
-  const int last = rt < s.q / sp.tpt ? (rt + 1) * sp.tpt : s.q;  // tokens up to this tile's end
-  return max(0, s.n - s.q + last);
-}
+// The tiles that hold the keys the last row of row tile rt sees.
 __device__ __forceinline__ int chunk_tiles(const ChunkSpace& sp, const ChunkSeq& s, int rt) {
-  return max(1, (chunk_kend(sp, s, rt) + kChunkKeys - 1) / kChunkKeys);
+  const int kend = sp.causal ? s.n - s.q + min(s.q, (rt + 1) * sp.tpt) : s.n;
+  return max(1, (kend + kChunkKeys - 1) / kChunkKeys);
 }
-__device__ __forceinline__ int chunk_row_tiles(const ChunkSpace& sp, const ChunkSeq& s) {
-  return (s.q + sp.tpt - 1) / sp.tpt;
+
+// sum of ceil((a + i T) / 64) over i = 1 .. m, for a >= 0: with i = 64 u + v, the
+// terms of a whole period of 64 rise by T from one period to the next. T a divisor
+// or multiple of 64 (any power of two) has a shorter one.
+__device__ __forceinline__ long long chunk_ceil_sum(int a, int T, int m) {
+  const int period = T >= 64 ? (T % 64 == 0 ? 1 : 64) : (64 % T == 0 ? 64 / T : 64);
+  const int rise = period * T / 64;  // of a term, one period later
+  const int u = m / period, v = m - u * period;
+  long long sum = 0;
+  for (int i = 1; i <= min(m, period); ++i) {
+    const long long first = (a + (long long)i * T + 63) / 64;
+    const long long terms = u + (i <= v ? 1 : 0);
+    sum += terms * first + rise * (terms * (terms - 1) / 2);
+  }
+  return sum;
 }
-// The length of one kv head's items of a sequence.
-__device__ __forceinline__ long long chunk_seq_cost(const ChunkSpace& sp, const ChunkSeq& s) {
-  const int nrt = chunk_row_tiles(sp, s);
-  long long c = 0;
-  for (int rt = 0; rt < nrt; ++rt) c += chunk_tiles(sp, s, rt) + kChunkItemCost;
+
+// The length of the first m items of one kv head of a sequence. A loop where
+// some rows see no key (more new tokens than keys).
+__device__ __forceinline__ long long chunk_cost(const ChunkSpace& sp, const ChunkSeq& s, int m) {
+  if (!sp.causal) return m * (long long)(chunk_tiles(sp, s, 0) + kChunkItemCost);
+  long long c = (long long)m * kChunkItemCost;
+  if (s.n < s.q) {
+    for (int rt = 0; rt < m; ++rt) c += chunk_tiles(sp, s, rt);
+    return c;
+  }
+  const int whole = m == s.nrt && m > 0 ? m - 1 : m;  // the last may be cut short
+  c += chunk_ceil_sum(s.n - s.q, sp.tpt, whole);
+  if (whole < m) c += chunk_tiles(sp, s, whole);
   return c;
 }
 
@@ -80,8 +99,8 @@ struct ChunkRange {
 };
 
 // Warp-cooperative, no barrier: each lane sums a contiguous chunk of the
-// sequences, a scan gives the prefix, and the lane whose chunk holds lo walks
-// to the item there.
+// sequences, a scan gives the prefix, the lane whose chunk holds lo finds the
+// sequence, and the lanes together its row tile.
 __device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
   const int lane = threadIdx.x & 31;
   const int chunk = (sp.B + 31) / 32;
@@ -89,8 +108,9 @@ __device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
   long long local = 0;
   int clamped = 0;
   for (int b = b0; b < b1; ++b) {
+    const ChunkSeq s = chunk_seq(sp, b);
     clamped |= chunk_seq_clamped(sp, b);
-    local += chunk_seq_cost(sp, chunk_seq(sp, b)) * sp.Hkv;
+    local += chunk_cost(sp, s, s.nrt) * sp.Hkv;
   }
   long long incl = local;
 #pragma unroll
@@ -106,36 +126,38 @@ __device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
   r.lo = min(total, (long long)c * r.per);
   r.hi = min(total, r.lo + r.per);
   long long pos = incl - local;
-  int fb = -1, fg = 0, frt = 0, foff = 0;
+  int fb = -1;
   if (r.lo < r.hi && r.lo >= pos && r.lo < incl) {
-    for (int b = b0; b < b1; ++b) {
-      const ChunkSeq s = chunk_seq(sp, b);
-      const long long w = chunk_seq_cost(sp, s);
-      if (r.lo < pos + w * sp.Hkv) {
-        long long rem = r.lo - pos;
-        fb = b;
-        fg = (int)div_pos(rem, w);
-        rem -= w * fg;
-        const int nrt = chunk_row_tiles(sp, s);
-        for (; frt + 1 < nrt; ++frt) {
-          const int len = chunk_tiles(sp, s, frt) + kChunkItemCost;
-          if (rem < len) break;
-          rem -= len;
-        }
-        foff = (int)rem;
-        break;
+    fb = b0;
+    if (b1 - b0 > 1) {
+      for (; fb < b1; ++fb) {
+        const ChunkSeq s = chunk_seq(sp, fb);
+        const long long w = chunk_cost(sp, s, s.nrt) * sp.Hkv;
+        if (r.lo < pos + w) break;
+        pos += w;
       }
-      pos += w * sp.Hkv;
     }
   }
   const unsigned owner = __ballot_sync(0xffffffffu, fb >= 0);
   if (owner) {
     const int src = __ffs(owner) - 1;
     r.b = __shfl_sync(0xffffffffu, fb, src);
-    r.g = __shfl_sync(0xffffffffu, fg, src);
-    r.rt = __shfl_sync(0xffffffffu, frt, src);
-    r.off = __shfl_sync(0xffffffffu, foff, src);
     r.s = chunk_seq(sp, r.b);
+    long long rem = r.lo - __shfl_sync(0xffffffffu, pos, src);
+    const long long w = chunk_cost(sp, r.s, r.s.nrt);
+    r.g = (int)div_pos(rem, w);
+    rem -= w * r.g;
+    // the largest rt with chunk_cost(rt) <= rem, in steps of 32 candidates
+    int lo = 0, hi = r.s.nrt;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
+      const bool below = i < hi && chunk_cost(sp, r.s, i) <= rem;
+      const int k = __ffs(~__ballot_sync(0xffffffffu, below) | 0x80000000u) - 1;
+      lo += k * step;
+      hi = min(hi, lo + step);
+    }
+    r.rt = lo;
+    r.off = (int)(rem - chunk_cost(sp, r.s, lo));
   }
   return r;
 }
@@ -173,7 +195,7 @@ struct ChunkCursor {
       off += take;
       if (off == len) {
         off = 0;
-        if (++rt == chunk_row_tiles(sp, s)) {
+        if (++rt >= s.nrt) {
           rt = 0;
           if (++g == sp.Hkv) {
             g = 0;

@@ -57,9 +57,20 @@ namespace plx {
 constexpr int kChThreads = 384;
 constexpr int kChConvertWarps = 2;
 
+// What the merge kernel does for one CTA: the item that ends in its range after
+// tiles in earlier ones. Written by the attention kernel, so that the merge
+// need not find the item again.
+struct alignas(16) ChunkMerge {
+  int token, ntok;      // first packed row and tokens of the row tile; ntok 0: nothing
+  int g;                // kv head
+  int c0, c0_first;     // the range of its first tile, and whether that is a first piece
+  int pad[3];
+};
+
 struct ChunkParams {
   ChunkSpace sp;
   __nv_bfloat16* out;      // [total][Hq][D]
+  ChunkMerge* merges;      // one per CTA
   float* records;          // 2 * gridDim.x partial records
   unsigned int* status;
   const int32_t* table;    // [B][max_pages]
@@ -166,6 +177,21 @@ __global__ void __launch_bounds__(kChThreads, 1)
   const ChunkRange range = chunk_locate(p.sp, (int)blockIdx.x, (int)gridDim.x);
   if (blockIdx.x == 0 && tid == 0 && range.clamped)
     atomicOr(p.status, 2u /* PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED */);
+  if (tid == 8 * 32) {
+    ChunkMerge mg{};
+    const int len =
+        range.lo < range.hi ? chunk_tiles(p.sp, range.s, range.rt) + kChunkItemCost : 0;
+    // some of the item's tiles come before this range, and its last one in it
+    if (len > 0 && range.off > kChunkItemCost && len - range.off <= range.hi - range.lo) {
+      const long long start = range.lo - range.off;
+      mg.token = range.s.s0 + range.rt * p.sp.tpt;
+      mg.ntok = min(p.sp.tpt, range.s.q - range.rt * p.sp.tpt);
+      mg.g = range.g;
+      mg.c0 = (int)div_pos(start + kChunkItemCost, range.per);
+      mg.c0_first = (long long)mg.c0 * range.per >= start;
+    }
+    p.merges[blockIdx.x] = mg;
+  }
   ChunkCursor cur(range);
   ChunkPiece pc;
   // Every role walks the same pieces and counts tiles over all of them: tile
@@ -763,33 +789,25 @@ __global__ void __launch_bounds__(kChThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, kPfTmemCols);
 }
 
-// Combines the partial records of every cut item: block (c, y) owns the item
-// that ends in range c after tiles in an earlier one, and merges slice y of
-// its columns (kChunkMergeCols float4 columns of A and of C), one row per
-// thread, the records in order:
+// Combines the partial records of every cut item: block (c, y) merges slice y of
+// the columns (kChunkMergeCols float4 columns of A and of C) of the item that
+// ends in range c, one row per thread, the records in order:
 //   M = max_j m_j, w_j = 2^(m_j - M), sums of w_j (l_j, b_j, A_j, C_j).
 constexpr int kChunkMergeCols = 2;
 
 template <int D, bool PROBE>
 __global__ void __launch_bounds__(kChunkRows) parallax_chunk_merge_kernel(const ChunkParams p) {
   const float kNegInf = __int_as_float(0xff800000u);
+  const int c = (int)blockIdx.x, r = threadIdx.x, r_tok = r / p.G, r_head = r - r_tok * p.G;
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int c = (int)blockIdx.x, P = (int)gridDim.x;
-  const ChunkRange rg = chunk_locate(p.sp, c, P);
-  if (rg.lo >= rg.hi || rg.off <= kChunkItemCost) return;  // no tile of it before this range
-  const int len = chunk_tiles(p.sp, rg.s, rg.rt) + kChunkItemCost;
-  if (len - rg.off > rg.hi - rg.lo) return;  // it ends in a later range
-  const long long start = rg.lo - rg.off;
-  // the range that holds the item's first tile
-  const int c0 = (int)div_pos(start + kChunkItemCost, rg.per);
-  const bool c0_first = (long long)c0 * rg.per >= start;
-  const int j0 = rg.rt * p.sp.tpt, ntok = min(p.sp.tpt, rg.s.q - j0);
-  const int r = threadIdx.x, r_tok = r / p.G, r_head = r - r_tok * p.G;
+  const int4* const mp = reinterpret_cast<const int4*>(p.merges + c);
+  const int4 m0 = __ldcg(mp), m1 = __ldcg(mp + 1);
+  const int token = m0.x, ntok = m0.y, g = m0.z, c0 = m0.w;
+  const bool c0_first = m1.x != 0;
   if (r_tok >= ntok) return;
   const auto record = [&](int j) {
-    return p.records +
-           (size_t)piece_slot(j, j > c0 || c0_first) * chunk_rec_floats(D);
+    return p.records + (size_t)piece_slot(j, j > c0 || c0_first) * chunk_rec_floats(D);
   };
   float M = kNegInf;
   for (int j = c0; j <= c; ++j) M = fmaxf(M, __ldcg(record(j) + r));
@@ -818,7 +836,7 @@ __global__ void __launch_bounds__(kChunkRows) parallax_chunk_merge_kernel(const 
   }
   const float inv = l > 0.f ? 1.f / l : 0.f, bl = b * inv;
   __nv_bfloat16* const out =
-      p.out + ((size_t)(rg.s.s0 + j0 + r_tok) * p.Hq + (size_t)rg.g * p.G + r_head) * D;
+      p.out + ((size_t)(token + r_tok) * p.Hq + (size_t)g * p.G + r_head) * D;
   const auto fin = [&](float a, float x) {
     const float vbar = a * inv;
     return PROBE ? vbar + (x * inv - bl * vbar) : vbar;
