@@ -298,13 +298,13 @@ struct NrUnits {
   __device__ void next() { unit = unit + stride < unit ? count : unit + stride; }
 };
 
-// 4 KB of rows per stage: 16 heads of 128 bf16 dimensions. Three blocks per SM.
-using NrForwardRing = NrRing<1, 4096, 2>;
+// 4 KB of rows per stage: 16 heads of 128 bf16 dimensions. Two blocks per SM.
+using NrForwardRing = NrRing<1, 4096, 3>;
 // 2 KB of dy and as much of x. Two blocks per SM.
 using NrBackwardRing = NrRing<2, 2048, 3>;
 
 template <typename T, int D, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kNrThreads, 3)
+__global__ void __launch_bounds__(kNrThreads, 2)
     parallax_norm_rope_kernel(const NormRopeParams p) {
   using Ring = NrForwardRing;
   constexpr int kLanes = D / 16, kGroups = 32 / kLanes, kSt = Ring::kStages;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kNrThreads, 3)
       }
       T* out = y + (size_t)out_row * D + (size_t)(h0 + grp) * head_step;
       const T* row = reinterpret_cast<const T*>(ring.rows(st, 0)) + grp * D;
-#pragma unroll 1
+#pragma unroll 2
       for (int h = grp; h < n + grp; h += kGroups) {  // the warp's groups together
         f32x2 a[4], b[4];
         nr_get(row + 8 * ln.a, a);  // past the unit's rows: stale, not stored

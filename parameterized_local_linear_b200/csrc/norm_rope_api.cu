@@ -81,7 +81,7 @@ void deal_blocks(NormRopeParams& p, int kinds, int most, int D, int stage_rows, 
   }
 }
 
-constexpr int kNrForwardBlocksPerSm = 3;
+constexpr int kNrForwardBlocksPerSm = 2;
 constexpr double kNrForwardUnitCost = 1.5;
 constexpr int kNrBackwardBlocksPerSm = 2;
 
