@@ -73,6 +73,7 @@ struct NormRopeParams {
   // append
   const int32_t *cu, *lens, *table;
   int B, page_size, num_pages, max_pages;
+  NrDivisor page_div;     // by page_size
   // backward: dy in the layout of y, dx rows dxs[i] elements apart
   const void* dy[3];
   void* dx[3];
@@ -237,23 +238,64 @@ __device__ __forceinline__ const float* nr_table_row(const NormRopeParams& p, lo
   return p.cs + (size_t)pos * p.rot;
 }
 
-// The sequence of packed row t: the largest b with cu[b] <= t < cu[b + 1], or
-// -1 outside every sequence. Warp-cooperative (one 32-way step per 32 x),
-// bounded for any contents of cu.
-__device__ __forceinline__ int nr_find_sequence(const int32_t* cu, int B, int t) {
-  const int lane = threadIdx.x & 31;
-  if (t < __ldg(cu) || t >= __ldg(cu + B)) return -1;
-  int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + (lane + 1) * step;
-    const bool below = i < hi && __ldg(cu + i) <= t;
-    const int n = __ffs(~__ballot_sync(0xffffffffu, below) | 0x80000000u) - 1;
-    lo += n * step;
-    hi = min(hi, lo + step);
+// The sequences of an append's packed rows. Up to 32 of them are kept by the
+// warp, one per lane; more are searched in memory.
+struct NrBatch {
+  int end, len, begin;  // cu[lane + 1], lens[lane], cu[0]
+  __device__ NrBatch(const int32_t* cu, const int32_t* lens, int B) : end(0x7fffffff), len(0), begin(0) {
+    const int lane = threadIdx.x & 31;
+    if (cu != nullptr && B <= 32) {
+      begin = __ldg(cu);
+      if (lane < B) {
+        end = __ldg(cu + lane + 1);
+        len = __ldg(lens + lane);
+      }
+    }
   }
-  return lo;
-}
+  // The key index that row t becomes and (slot) its sequence; slot -1 and key -1
+  // outside every sequence. A key below 0 or past the table is not stored; the
+  // caller sees it by the page it then lacks.
+  __device__ long long key(const int32_t* cu, const int32_t* lens, int B, int t, int& b) const {
+    if (cu == nullptr) {
+      b = t;
+      return (long long)__ldg(lens + t) - 1;
+    }
+    int last, n;
+    if (B <= 32) {
+      // the largest b with cu[b] <= t < cu[b + 1]: as many ends in a row are <= t
+      const unsigned past = __ballot_sync(0xffffffffu, end <= t);
+      b = past == 0xffffffffu ? 32 : __ffs(~past) - 1;
+      if (t < begin || b >= B) {
+        b = -1;
+        return -1;
+      }
+      last = __shfl_sync(0xffffffffu, end, b);
+      n = __shfl_sync(0xffffffffu, len, b);
+    } else {
+      b = search(cu, B, t);
+      if (b < 0) return -1;
+      last = __ldg(cu + b + 1);
+      n = __ldg(lens + b);
+    }
+    return (long long)n - last + t;
+  }
+  // The largest b with cu[b] <= t < cu[b + 1], or -1. Warp-cooperative (one
+  // 32-way step per 32 x), bounded for any contents of cu.
+  static __device__ int search(const int32_t* cu, int B, int t) {
+    const int lane = threadIdx.x & 31;
+    if (t < __ldg(cu) || t >= __ldg(cu + B)) return -1;
+    int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32;
+      const int i = lo + (lane + 1) * step;
+      const bool below = i < hi && __ldg(cu + i) <= t;
+      const int n = __ffs(~__ballot_sync(0xffffffffu, below) | 0x80000000u) - 1;
+      lo += n * step;
+      hi = min(hi, lo + step);
+    }
+    return lo;
+  }
+};
 
 // The ring of one warp: kStages stages of PARTS x BYTES of head rows, a table
 // row (up to 512 bytes) and a note, filled by bulk copies that an mbarrier per
@@ -330,6 +372,34 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   pdl_launch_dependents();
   NrUnits at(blk * kNrWarps + warp, nblk * kNrWarps, p.tokens, p.unit_div[k], p.unit_rows),
       load_at = at;
+  const NrBatch batch(APPEND ? p.cu : nullptr, APPEND ? p.lens : nullptr, p.B);
+  // A unit's place, looked up one unit ahead, so that no load is waited for when
+  // its copies start: its position, and (append) the page that takes its key.
+  struct Place {
+    int pos, page, slot;  // slot -1: a padding row; page and slot of kinds 2, 3
+  };
+  const auto look_up = [&](const NrUnits& u) {
+    Place f{0, -1, -1};
+    if (!u.valid()) return f;
+    int t, h0;
+    u.place(t, h0);
+    long long key = t;
+    f.slot = 0;
+    if (APPEND) {
+      key = batch.key(p.cu, p.lens, p.B, t, f.slot);
+      if (k >= 2 && key >= 0 && key < (long long)p.max_pages * p.page_size) {
+        const int i = p.page_div.quotient((int)key);
+        f.page = __ldg(p.table + (size_t)f.slot * p.max_pages + i);
+        f.slot = (int)key - i * p.page_size;
+      }
+    } else if (p.seq_len > 0) {
+      key = t - p.seq_div.quotient(t) * p.seq_len;
+    }
+    f.pos = (int)max(-1LL, min(key, 0x7fffffffLL));  // (outside the table: clamped below)
+    if (p.pos != nullptr && k < 3 && f.slot >= 0) f.pos = __ldg(p.pos + t);
+    return f;
+  };
+  Place ahead = look_up(load_at);
   // Starts the copies of the next unit. Its note: the first row (in units of D
   // elements) of its token's heads in the output, or -1 where it has none.
   const auto load = [&](int st) {
@@ -337,45 +407,29 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     int t, h0;
     load_at.place(t, h0);
     load_at.next();
+    const Place f = ahead;
     const uint32_t bytes = (uint32_t)(min(load_at.rows, H - h0) * kRowBytes);
     if (lane == 0) {
       mbar_arrive_expect_tx(ring.bar(st), bytes + (k < 3 ? p.rot * 4 : 0));
       bulk_load(smem_u32(ring.rows(st, 0)), x + (size_t)t * xs + (size_t)h0 * D, bytes,
                 ring.bar(st));
-    }
-    long long pos = t, note;
-    if (APPEND) {
-      int b = t;
-      if (p.cu != nullptr) b = nr_find_sequence(p.cu, p.B, t);
-      note = b < 0 ? -1 : (long long)t * H;  // -1: a padding row, left as it is
-      if (b >= 0 && (k >= 2 || p.pos == nullptr)) {
-        pos = (long long)__ldg(p.lens + b) - 1;
-        if (p.cu != nullptr) pos += t + 1 - __ldg(p.cu + b + 1);
-        if (k >= 2) {  // the key's place in the pools
-          note = -1;
-          if (pos >= 0 && pos < (long long)p.max_pages * p.page_size) {
-            const int page = __ldg(p.table + (size_t)b * p.max_pages + (int)pos / p.page_size);
-            if (page >= 0 && page < p.num_pages)
-              note = ((long long)page * p.page_size + (int)pos % p.page_size) * H;
-          }
-          if (note < 0 && lane == 0) atomicOr(p.status, kNrStatusClamped);
-        }
+      long long note = (long long)t * H;
+      if (APPEND && f.slot < 0) {
+        note = -1;
+      } else if (APPEND && k >= 2) {  // the key's place in the pools
+        const bool held = f.page >= 0 && f.page < p.num_pages;
+        note = held ? ((long long)f.page * p.page_size + f.slot) * H : -1;
+        if (!held) atomicOr(p.status, kNrStatusClamped);
+      } else if (!APPEND && p.seq_len > 0) {
+        const int row = p.seq_div.quotient(t);
+        note = (long long)row * H * p.seq_len + (t - row * p.seq_len);
       }
-    } else if (p.seq_len > 0) {
-      const int row = p.seq_div.quotient(t), i = t - row * p.seq_len;
-      pos = i;
-      note = (long long)row * H * p.seq_len + i;
-    } else {
-      note = (long long)t * H;
-    }
-    if (lane == 0) {
-      if (k < 3) {
-        if (p.pos != nullptr) pos = note >= 0 ? __ldg(p.pos + t) : 0;
-        if (note < 0) pos = max(0LL, min(pos, (long long)p.max_pos - 1));
-        bulk_load(smem_u32(ring.table(st)), nr_table_row(p, pos), p.rot * 4, ring.bar(st));
-      }
+      if (k < 3)
+        bulk_load(smem_u32(ring.table(st)), f.slot < 0 ? p.cs : nr_table_row(p, f.pos), p.rot * 4,
+                  ring.bar(st));
       *ring.note(st) = note;
     }
+    ahead = look_up(load_at);
   };
 #pragma unroll 1
   for (int st = 0; st < kSt; ++st) load(st);
@@ -481,17 +535,24 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   pdl_launch_dependents();
   NrUnits at(blk * kNrWarps + warp, nblk * kNrWarps, p.tokens, p.unit_div[k], p.unit_rows),
       load_at = at;
+  const auto position = [&](const NrUnits& u) {  // looked up one unit ahead
+    int t, h0;
+    u.place(t, h0);
+    if (p.pos != nullptr) return u.valid() ? __ldg(p.pos + t) : 0;
+    return p.seq_len > 0 ? t - p.seq_div.quotient(t) * p.seq_len : t;
+  };
+  int ahead = position(load_at);
   const auto load = [&](int st) {
     if (!load_at.valid()) return;
     int t, h0;
     load_at.place(t, h0);
     load_at.next();
+    const int pos = ahead;
     const int n = min(load_at.rows, H - h0);
     const uint32_t bytes = (uint32_t)(n * kRowBytes);
-    long long pos = t, dy_row = (long long)t * H + h0;
+    long long dy_row = (long long)t * H + h0;
     if (p.seq_len > 0) {
       const int row = p.seq_div.quotient(t), i = t - row * p.seq_len;
-      pos = i;
       dy_row = ((long long)row * H + h0) * p.seq_len + i;
     }
     if (lane == 0) {
@@ -499,7 +560,6 @@ __global__ void __launch_bounds__(kNrThreads, 2)
       if (norm)
         bulk_load(smem_u32(ring.rows(st, 1)), x + (size_t)t * xs + (size_t)h0 * D, bytes,
                   ring.bar(st));
-      if (p.pos != nullptr) pos = __ldg(p.pos + t);
       if (p.seq_len == 0)
         bulk_load(smem_u32(ring.rows(st, 0)), dy + (size_t)dy_row * D, bytes, ring.bar(st));
       bulk_load(smem_u32(ring.table(st)), nr_table_row(p, pos), p.rot * 4, ring.bar(st));
@@ -510,6 +570,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
         bulk_load(smem_u32(ring.rows(st, 0)) + lane * kRowBytes,
                   dy + (size_t)(dy_row + (long long)lane * p.seq_len) * D, kRowBytes, ring.bar(st));
     }
+    ahead = position(load_at);
   };
 #pragma unroll 1
   for (int st = 0; st < kSt; ++st) load(st);
@@ -533,7 +594,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     T* out = dx + (size_t)t * dxs + (size_t)(h0 + grp) * D;
     const T* gr = reinterpret_cast<const T*>(ring.rows(st, 0)) + grp * D;
     const T* xr = reinterpret_cast<const T*>(ring.rows(st, 1)) + grp * D;
-#pragma unroll 1
+#pragma unroll 2
     for (int h = grp; h < n + grp; h += kGroups) {  // the warp's groups together
       f32x2 ga[4], gb[4], a[4], b[4];
       const bool live = h < n;

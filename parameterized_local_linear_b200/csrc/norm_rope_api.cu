@@ -296,6 +296,7 @@ extern "C" int parallax_norm_rope_append(
   p.table = block_table;
   p.B = B;
   p.page_size = page_size;
+  p.page_div = NrDivisor::of(page_size);
   p.num_pages = num_pages;
   p.max_pages = max_pages_per_seq;
   return dispatch_forward<true>(p, D, interleaved, dtype, static_cast<cudaStream_t>(stream));
