@@ -34,7 +34,6 @@ struct ChunkSpace {
 
 struct ChunkSeq {
   int s0, q, n;  // first packed row, new tokens, cached keys
-  int nrt;       // row tiles
 };
 
 __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
@@ -42,8 +41,11 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
   s.s0 = min(max(__ldg(sp.cu + b), 0), sp.total);
   s.q = min(max(__ldg(sp.cu + b + 1), s.s0), sp.total) - s.s0;
   s.n = clamp_len(__ldg(sp.lens + b), sp.Lmax);
-  s.nrt = (s.q + sp.tpt - 1) / sp.tpt;
   return s;
+}
+
+__device__ __forceinline__ int chunk_row_tiles(const ChunkSpace& sp, const ChunkSeq& s) {
+  return (s.q + sp.tpt - 1) / sp.tpt;
 }
 
 // A sequence whose bounds or length chunk_seq clamped, or with more new tokens
@@ -84,7 +86,7 @@ __device__ __forceinline__ long long chunk_cost(const ChunkSpace& sp, const Chun
     for (int rt = 0; rt < m; ++rt) c += chunk_tiles(sp, s, rt);
     return c;
   }
-  const int whole = m == s.nrt && m > 0 ? m - 1 : m;  // the last may be cut short
+  const int whole = m > 0 && m == chunk_row_tiles(sp, s) ? m - 1 : m;  // the last may be cut short
   c += chunk_ceil_sum(s.n - s.q, sp.tpt, whole);
   if (whole < m) c += chunk_tiles(sp, s, whole);
   return c;
@@ -110,7 +112,7 @@ __device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
   for (int b = b0; b < b1; ++b) {
     const ChunkSeq s = chunk_seq(sp, b);
     clamped |= chunk_seq_clamped(sp, b);
-    local += chunk_cost(sp, s, s.nrt) * sp.Hkv;
+    local += chunk_cost(sp, s, chunk_row_tiles(sp, s)) * sp.Hkv;
   }
   long long incl = local;
 #pragma unroll
@@ -132,7 +134,7 @@ __device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
     if (b1 - b0 > 1) {
       for (; fb < b1; ++fb) {
         const ChunkSeq s = chunk_seq(sp, fb);
-        const long long w = chunk_cost(sp, s, s.nrt) * sp.Hkv;
+        const long long w = chunk_cost(sp, s, chunk_row_tiles(sp, s)) * sp.Hkv;
         if (r.lo < pos + w) break;
         pos += w;
       }
@@ -144,11 +146,11 @@ __device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
     r.b = __shfl_sync(0xffffffffu, fb, src);
     r.s = chunk_seq(sp, r.b);
     long long rem = r.lo - __shfl_sync(0xffffffffu, pos, src);
-    const long long w = chunk_cost(sp, r.s, r.s.nrt);
+    const long long w = chunk_cost(sp, r.s, chunk_row_tiles(sp, r.s));
     r.g = (int)div_pos(rem, w);
     rem -= w * r.g;
     // the largest rt with chunk_cost(rt) <= rem, in steps of 32 candidates
-    int lo = 0, hi = r.s.nrt;
+    int lo = 0, hi = chunk_row_tiles(sp, r.s);
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
       const bool below = i < hi && chunk_cost(sp, r.s, i) <= rem;
@@ -195,7 +197,7 @@ struct ChunkCursor {
       off += take;
       if (off == len) {
         off = 0;
-        if (++rt >= s.nrt) {
+        if (++rt >= chunk_row_tiles(sp, s)) {
           rt = 0;
           if (++g == sp.Hkv) {
             g = 0;

@@ -137,7 +137,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gbase + kOffMisc + 20 * kSt);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(gbase + kOffMisc + 20 * kSt + 4);
   float* const red = reinterpret_cast<float*>(gbase + Geo::kOffRed);
-  static_assert(kOffMisc % 16 == 0 && 16 + 5 * 8 * kSt + 64 + 20 * kSt + 8 <= 512, "misc area");
+  ChunkRange* const range_slot = reinterpret_cast<ChunkRange*>(gbase + kOffMisc + 20 * kSt + 16);
+  static_assert(kOffMisc % 16 == 0 &&
+                    16 + 5 * 8 * kSt + 64 + 20 * kSt + 16 + sizeof(ChunkRange) <= 512,
+                "misc area");
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be warp-uniform
@@ -174,24 +177,30 @@ __global__ void __launch_bounds__(kChThreads, 1)
   pdl_wait_primary();  // nothing above reads global memory
   pdl_launch_dependents();
 
-  const ChunkRange range = chunk_locate(p.sp, (int)blockIdx.x, (int)gridDim.x);
-  if (blockIdx.x == 0 && tid == 0 && range.clamped)
-    atomicOr(p.status, 2u /* PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED */);
-  if (tid == 8 * 32) {
-    ChunkMerge mg{};
-    const int len =
-        range.lo < range.hi ? chunk_tiles(p.sp, range.s, range.rt) + kChunkItemCost : 0;
-    // some of the item's tiles come before this range, and its last one in it
-    if (len > 0 && range.off > kChunkItemCost && len - range.off <= range.hi - range.lo) {
-      const long long start = range.lo - range.off;
-      mg.token = range.s.s0 + range.rt * p.sp.tpt;
-      mg.ntok = min(p.sp.tpt, range.s.q - range.rt * p.sp.tpt);
-      mg.g = range.g;
-      mg.c0 = (int)div_pos(start + kChunkItemCost, range.per);
-      mg.c0_first = (long long)mg.c0 * range.per >= start;
+  // one warp finds this CTA's range, the roles take it from shared memory
+  if (warp == 8) {
+    const ChunkRange range = chunk_locate(p.sp, (int)blockIdx.x, (int)gridDim.x);
+    if (lane == 0) {
+      *range_slot = range;
+      if (blockIdx.x == 0 && range.clamped)
+        atomicOr(p.status, 2u /* PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED */);
+      ChunkMerge mg{};
+      const int len =
+          range.lo < range.hi ? chunk_tiles(p.sp, range.s, range.rt) + kChunkItemCost : 0;
+      // some of the item's tiles come before this range, and its last one in it
+      if (len > 0 && range.off > kChunkItemCost && len - range.off <= range.hi - range.lo) {
+        const long long start = range.lo - range.off;
+        mg.token = range.s.s0 + range.rt * p.sp.tpt;
+        mg.ntok = min(p.sp.tpt, range.s.q - range.rt * p.sp.tpt);
+        mg.g = range.g;
+        mg.c0 = (int)div_pos(start + kChunkItemCost, range.per);
+        mg.c0_first = (long long)mg.c0 * range.per >= start;
+      }
+      p.merges[blockIdx.x] = mg;
     }
-    p.merges[blockIdx.x] = mg;
   }
+  __syncthreads();
+  const ChunkRange range = *range_slot;
   ChunkCursor cur(range);
   ChunkPiece pc;
   // Every role walks the same pieces and counts tiles over all of them: tile
