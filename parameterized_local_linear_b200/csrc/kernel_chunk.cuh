@@ -494,211 +494,228 @@ __global__ void __launch_bounds__(kChThreads, 1)
       };
       const int lim_a = row_limit(tok_a), lim_b = row_limit(tok_b), kall = min(pc.s.n, seen0);
       Row A{kNegInf, 0.f, 0.f, 0.f, 0.f}, B = A;
-      for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
-        const int st = jt % kSt;
-        // the tile's V is ready, and its flags with it, before its scores are
-        ok = mbar_wait_bounded(v_ready + 8 * st, round_parity(jt), p.timeout_ns, abort_flag);
-        const int4 vi = v_info[st];
-        const bool in_pool = (vi.x & 2) != 0;
-        const bool f16 = (vi.x & vi.y & vi.z & vi.w & 1) != 0;
-        ok = ok && mbar_wait_bounded(s_full, jt & 1, p.timeout_ns, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        float sv[32], tv[32];
-        tmem_ld16x64(t16 + kPfColS, sv);
-        if constexpr (PROBE) tmem_ld16x64(t16 + kPfColT, tv);
-        // S_j, T_j complete: the score UMMAs have read K_j, and the value UMMAs
-        // of tile j - 2, issued before them, V and P of that tile
-        if (warp == 0 && lane == 0) {
-          mbar_arrive(k_empty + 8 * st);
-          for (; freed < jt - 1; ++freed) mbar_arrive(v_empty + 8 * (freed % kSt));
-        }
-        tmem_wait_ld();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
-        // mask
-        const int k0 = j * kChunkKeys;
-        if (!(in_pool && k0 + kChunkKeys <= kall)) {
-          const int la = in_pool ? lim_a - k0 - col : 0, lb = in_pool ? lim_b - k0 - col : 0;
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const bool own = 8 * (x >> 2) + (x & 1) < ((x & 2) ? lb : la);
-            sv[x] = own ? sv[x] : kNegInf;
-            if constexpr (PROBE) tv[x] = own ? tv[x] : 0.f;
+      // A warp whose rows are all past the tile's tokens only keeps the barriers'
+      // pace: the products of its rows are not used, whatever P holds there. With
+      // few rows the others then have the schedulers for themselves.
+      if ((quarter * 32 + half * 16) / p.G >= ntok) {
+        for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
+          ok = mbar_wait_bounded(s_full, jt & 1, p.timeout_ns, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive(s_free);
+            mbar_arrive(p_full + 8 * (jt & 1));
           }
         }
-        // Lazy rescale: keep the stale max unless this tile exceeds it by 2^4,
-        // and 2^sigma unless |s| 2^sigma reaches 2^11.
-        const auto within = [&](const Row& w, float mx, float sx) {
-          return mx * c <= w.m + 4.f && (!PROBE || (sx * w.s_scale < 2048.f && w.s_scale > 0.f));
-        };
-        float alpha[2] = {1.f, 1.f}, alpha_c[2] = {1.f, 1.f};  // factors of l, A and of b, C
-        const auto update = [&](float ma, float mb, float sa, float sb) {
+      } else {
+        for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
+          const int st = jt % kSt;
+          // the tile's V is ready, and its flags with it, before its scores are
+          ok = mbar_wait_bounded(v_ready + 8 * st, round_parity(jt), p.timeout_ns, abort_flag);
+          const int4 vi = v_info[st];
+          const bool in_pool = (vi.x & 2) != 0;
+          const bool f16 = (vi.x & vi.y & vi.z & vi.w & 1) != 0;
+          ok = ok && mbar_wait_bounded(s_full, jt & 1, p.timeout_ns, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          float sv[32], tv[32];
+          tmem_ld16x64(t16 + kPfColS, sv);
+          if constexpr (PROBE) tmem_ld16x64(t16 + kPfColT, tv);
+          // S_j, T_j complete: the score UMMAs have read K_j, and the value UMMAs
+          // of tile j - 2, issued before them, V and P of that tile
+          if (warp == 0 && lane == 0) {
+            mbar_arrive(k_empty + 8 * st);
+            for (; freed < jt - 1; ++freed) mbar_arrive(v_empty + 8 * (freed % kSt));
+          }
+          tmem_wait_ld();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+          // mask
+          const int k0 = j * kChunkKeys;
+          if (!(in_pool && k0 + kChunkKeys <= kall)) {
+            const int la = in_pool ? lim_a - k0 - col : 0, lb = in_pool ? lim_b - k0 - col : 0;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const bool own = 8 * (x >> 2) + (x & 1) < ((x & 2) ? lb : la);
+              sv[x] = own ? sv[x] : kNegInf;
+              if constexpr (PROBE) tv[x] = own ? tv[x] : 0.f;
+            }
+          }
+          // Lazy rescale: keep the stale max unless this tile exceeds it by 2^4,
+          // and 2^sigma unless |s| 2^sigma reaches 2^11.
+          const auto within = [&](const Row& w, float mx, float sx) {
+            return mx * c <= w.m + 4.f && (!PROBE || (sx * w.s_scale < 2048.f && w.s_scale > 0.f));
+          };
+          float alpha[2] = {1.f, 1.f}, alpha_c[2] = {1.f, 1.f};  // factors of l, A and of b, C
+          const auto update = [&](float ma, float mb, float sa, float sb) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              Row& w = y ? B : A;
+              float mx = (y ? mb : ma) * c, sx = y ? sb : sa;  // (the scale is positive)
+#pragma unroll
+              for (int o = 1; o < 4; o <<= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                sx = fmaxf(sx, __shfl_xor_sync(0xffffffffu, sx, o));
+              }
+              float alpha_s = 1.f;
+              if (mx > w.m + 4.f) {
+                alpha[y] = w.m == kNegInf ? 0.f : ex2_approx(w.m - mx);
+                w.m = mx;
+              }
+              if (PROBE && !(sx * w.s_scale < 2048.f && w.s_scale > 0.f)) {
+                // sx 2^sigma in [2^8, 2^9): room to grow before the next change
+                const int ex = max((int)((__float_as_uint(sx) >> 23) & 0xffu) - 127, -100);
+                const float ns = __int_as_float((135 - ex) << 23);
+                alpha_s = ns * w.s_unscale;
+                w.s_scale = ns;
+                w.s_unscale = __int_as_float((119 + ex) << 23);
+              }
+              alpha_c[y] = alpha[y] * alpha_s;
+              w.l *= alpha[y];
+              w.b *= alpha_c[y];
+            }
+          };
+          const f32x2 c2 = f2_pack(c, c);
+          f32x2 lt[2], bt[2];  // per row: the sums of the even and the odd keys
+          f32x2 nm[2], ss[2];
+          const auto factors = [&]() {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const Row& w = y ? B : A;
+              const float neg_m = (w.m == kNegInf ? 0.f : -w.m) + 11.f;  // no key yet: e = 0
+              nm[y] = f2_pack(neg_m, neg_m);
+              const float sc = w.s_scale * (1.f / 2048.f);  // of e 2^11
+              ss[y] = f2_pack(sc, sc);
+              lt[y] = bt[y] = 0;
+            }
+          };
+          // fp16 weights of the 32 values
+          uint32_t ph[16], th[PROBE ? 16 : 1];
+          const auto weights = [&]() {
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {  // pair u / 2 of row u % 2
+              const int y = u & 1;
+              float e0, e1;
+              ch_exp2(f2_pack(sv[2 * u], sv[2 * u + 1]), c2, nm[y], e0, e1);
+              ph[u] = pack_f16x2(e0, e1);
+              const f32x2 a = f2_pack(f16_lo_to_float(ph[u]), f16_hi_to_float(ph[u]));
+              lt[y] = f2_add(lt[y], a);
+              if constexpr (PROBE) {  // e s from the rounded e: the weights P applies
+                float x0, x1;
+                f2_unpack(f2_mul(f2_mul(a, ss[y]), f2_pack(tv[2 * u], tv[2 * u + 1])), x0, x1);
+                th[u] = pack_f16x2(x0, x1);
+                bt[y] = f2_add(bt[y], f2_pack(f16_lo_to_float(th[u]), f16_hi_to_float(th[u])));
+              }
+            }
+          };
+          float ma = sv[0], mb = sv[2], sa = 0.f, sb = 0.f;  // the largest t and |s| of both rows
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            ma = max3(ma, sv[x], sv[x + 1]);
+            mb = max3(mb, sv[x + 2], sv[x + 3]);
+            if constexpr (PROBE) {
+              sa = max3_abs(sa, tv[x], tv[x + 1]);
+              sb = max3_abs(sb, tv[x + 2], tv[x + 3]);
+            }
+          }
+          const bool grow =
+              __any_sync(0xffffffffu, !(within(A, ma, sa) && within(B, mb, sb)) && in_pool);
+          if (grow) update(ma, mb, sa, sb);  // (the row's four threads need a common value)
+          factors();
+          if (f16) weights();
+          // A tile of fp16 blocks alternates between two P buffers, and its buffer
+          // is free (above). One with hi + lo weights fills both. O may need a
+          // rescale. For either, the products of the tile before must be done.
+          const auto prev_done_and_rescale = [&]() -> bool {
+            const bool wait = j > pc.t0 && (grow || wide || !f16);
+            wide = !f16;
+            if (!wait) return true;
+            const bool got = mbar_wait_bounded(o_done, (jt - 1) & 1, p.timeout_ns, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) return false;
+            tc_fence_after_sync();
+            if (grow) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < (PROBE ? 2 * D : D); c0 += 64) {
+                const float fa = c0 < D ? alpha[0] : alpha_c[0], fb = c0 < D ? alpha[1] : alpha_c[1];
+                float o[32];
+                tmem_ld16x64(t16 + Geo::kColOA + c0, o);  // O_C follows O_A
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] *= (x & 2) ? fb : fa;
+                tmem_st16x64(t16 + Geo::kColOA + c0, o);
+              }
+            }
+            return true;
+          };
+          if (f16) {
+            if (!prev_done_and_rescale()) {
+              ok = false;
+              break;
+            }
+            tmem_st16x32u(t16 + kPfColP + 64 * (jt & 1), ph);
+            if constexpr (PROBE) tmem_st16x32u(t16 + kPfColP + 64 * (jt & 1) + 32, th);
+          } else {
+            if (!prev_done_and_rescale()) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {  // 16 keys: fp16, or bf16 hi + lo
+              const bool g16 = ((g == 0 ? vi.x : g == 1 ? vi.y : g == 2 ? vi.z : vi.w) & 1) != 0;
+              uint32_t hi[4], lo[4], thi[4], tlo[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int y = u & 1, x = 8 * g + 2 * u;
+                float e0, e1, t0 = 0.f, t1 = 0.f;
+                ch_exp2(f2_pack(sv[x], sv[x + 1]), c2, nm[y], e0, e1);
+                if constexpr (PROBE) f2_unpack(f2_mul(ss[y], f2_pack(tv[x], tv[x + 1])), t0, t1);
+                lo[u] = tlo[u] = 0;
+                if (g16) {
+                  hi[u] = pack_f16x2(e0, e1);
+                  e0 = f16_lo_to_float(hi[u]);
+                  e1 = f16_hi_to_float(hi[u]);
+                  thi[u] = pack_f16x2(e0 * t0, e1 * t1);
+                  t0 = f16_lo_to_float(thi[u]);
+                  t1 = f16_hi_to_float(thi[u]);
+                } else {
+                  e0 = round17(e0);
+                  e1 = round17(e1);
+                  split_hi_lo(e0, e1, hi[u], lo[u]);
+                  t0 = round17(e0 * t0);
+                  t1 = round17(e1 * t1);
+                  split_hi_lo(t0, t1, thi[u], tlo[u]);
+                }
+                lt[y] = f2_add(lt[y], f2_pack(e0, e1));
+                bt[y] = f2_add(bt[y], f2_pack(t0, t1));
+              }
+              tmem_st16x8u(t16 + kPfColP + 8 * g, hi);
+              tmem_st16x8u(t16 + kPfColP + 64 + 8 * g, lo);
+              if constexpr (PROBE) {
+                tmem_st16x8u(t16 + kPfColP + 32 + 8 * g, thi);
+                tmem_st16x8u(t16 + kPfColP + 96 + 8 * g, tlo);
+              }
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 8 * (jt & 1));
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             Row& w = y ? B : A;
-            float mx = (y ? mb : ma) * c, sx = y ? sb : sa;  // (the scale is positive)
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              sx = fmaxf(sx, __shfl_xor_sync(0xffffffffu, sx, o));
-            }
-            float alpha_s = 1.f;
-            if (mx > w.m + 4.f) {
-              alpha[y] = w.m == kNegInf ? 0.f : ex2_approx(w.m - mx);
-              w.m = mx;
-            }
-            if (PROBE && !(sx * w.s_scale < 2048.f && w.s_scale > 0.f)) {
-              // sx 2^sigma in [2^8, 2^9): room to grow before the next change
-              const int ex = max((int)((__float_as_uint(sx) >> 23) & 0xffu) - 127, -100);
-              const float ns = __int_as_float((135 - ex) << 23);
-              alpha_s = ns * w.s_unscale;
-              w.s_scale = ns;
-              w.s_unscale = __int_as_float((119 + ex) << 23);
-            }
-            alpha_c[y] = alpha[y] * alpha_s;
-            w.l *= alpha[y];
-            w.b *= alpha_c[y];
-          }
-        };
-        const f32x2 c2 = f2_pack(c, c);
-        f32x2 lt[2], bt[2];  // per row: the sums of the even and the odd keys
-        f32x2 nm[2], ss[2];
-        const auto factors = [&]() {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const Row& w = y ? B : A;
-            const float neg_m = (w.m == kNegInf ? 0.f : -w.m) + 11.f;  // no key yet: e = 0
-            nm[y] = f2_pack(neg_m, neg_m);
-            const float sc = w.s_scale * (1.f / 2048.f);  // of e 2^11
-            ss[y] = f2_pack(sc, sc);
-            lt[y] = bt[y] = 0;
-          }
-        };
-        // fp16 weights of the 32 values
-        uint32_t ph[16], th[PROBE ? 16 : 1];
-        const auto weights = [&]() {
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {  // pair u / 2 of row u % 2
-            const int y = u & 1;
-            float e0, e1;
-            ch_exp2(f2_pack(sv[2 * u], sv[2 * u + 1]), c2, nm[y], e0, e1);
-            ph[u] = pack_f16x2(e0, e1);
-            const f32x2 a = f2_pack(f16_lo_to_float(ph[u]), f16_hi_to_float(ph[u]));
-            lt[y] = f2_add(lt[y], a);
-            if constexpr (PROBE) {  // e s from the rounded e: the weights P applies
-              float x0, x1;
-              f2_unpack(f2_mul(f2_mul(a, ss[y]), f2_pack(tv[2 * u], tv[2 * u + 1])), x0, x1);
-              th[u] = pack_f16x2(x0, x1);
-              bt[y] = f2_add(bt[y], f2_pack(f16_lo_to_float(th[u]), f16_hi_to_float(th[u])));
-            }
-          }
-        };
-        float ma = sv[0], mb = sv[2], sa = 0.f, sb = 0.f;  // the largest t and |s| of both rows
-#pragma unroll
-        for (int x = 0; x < 32; x += 4) {
-          ma = max3(ma, sv[x], sv[x + 1]);
-          mb = max3(mb, sv[x + 2], sv[x + 3]);
-          if constexpr (PROBE) {
-            sa = max3_abs(sa, tv[x], tv[x + 1]);
-            sb = max3_abs(sb, tv[x + 2], tv[x + 3]);
-          }
-        }
-        const bool grow =
-            __any_sync(0xffffffffu, !(within(A, ma, sa) && within(B, mb, sb)) && in_pool);
-        if (grow) update(ma, mb, sa, sb);  // (the row's four threads need a common value)
-        factors();
-        if (f16) weights();
-        // A tile of fp16 blocks alternates between two P buffers, and its buffer
-        // is free (above). One with hi + lo weights fills both. O may need a
-        // rescale. For either, the products of the tile before must be done.
-        const auto prev_done_and_rescale = [&]() -> bool {
-          const bool wait = j > pc.t0 && (grow || wide || !f16);
-          wide = !f16;
-          if (!wait) return true;
-          const bool got = mbar_wait_bounded(o_done, (jt - 1) & 1, p.timeout_ns, abort_flag);
-          if (!__all_sync(0xffffffffu, got)) return false;
-          tc_fence_after_sync();
-          if (grow) {
-#pragma unroll 1
-            for (int c0 = 0; c0 < (PROBE ? 2 * D : D); c0 += 64) {
-              const float fa = c0 < D ? alpha[0] : alpha_c[0], fb = c0 < D ? alpha[1] : alpha_c[1];
-              float o[32];
-              tmem_ld16x64(t16 + Geo::kColOA + c0, o);  // O_C follows O_A
-              tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] *= (x & 2) ? fb : fa;
-              tmem_st16x64(t16 + Geo::kColOA + c0, o);
-            }
-          }
-          return true;
-        };
-        if (f16) {
-          if (!prev_done_and_rescale()) {
-            ok = false;
-            break;
-          }
-          tmem_st16x32u(t16 + kPfColP + 64 * (jt & 1), ph);
-          if constexpr (PROBE) tmem_st16x32u(t16 + kPfColP + 64 * (jt & 1) + 32, th);
-        } else {
-          if (!prev_done_and_rescale()) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {  // 16 keys: fp16, or bf16 hi + lo
-            const bool g16 = ((g == 0 ? vi.x : g == 1 ? vi.y : g == 2 ? vi.z : vi.w) & 1) != 0;
-            uint32_t hi[4], lo[4], thi[4], tlo[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int y = u & 1, x = 8 * g + 2 * u;
-              float e0, e1, t0 = 0.f, t1 = 0.f;
-              ch_exp2(f2_pack(sv[x], sv[x + 1]), c2, nm[y], e0, e1);
-              if constexpr (PROBE) f2_unpack(f2_mul(ss[y], f2_pack(tv[x], tv[x + 1])), t0, t1);
-              lo[u] = tlo[u] = 0;
-              if (g16) {
-                hi[u] = pack_f16x2(e0, e1);
-                e0 = f16_lo_to_float(hi[u]);
-                e1 = f16_hi_to_float(hi[u]);
-                thi[u] = pack_f16x2(e0 * t0, e1 * t1);
-                t0 = f16_lo_to_float(thi[u]);
-                t1 = f16_hi_to_float(thi[u]);
-              } else {
-                e0 = round17(e0);
-                e1 = round17(e1);
-                split_hi_lo(e0, e1, hi[u], lo[u]);
-                t0 = round17(e0 * t0);
-                t1 = round17(e1 * t1);
-                split_hi_lo(t0, t1, thi[u], tlo[u]);
-              }
-              lt[y] = f2_add(lt[y], f2_pack(e0, e1));
-              bt[y] = f2_add(bt[y], f2_pack(t0, t1));
-            }
-            tmem_st16x8u(t16 + kPfColP + 8 * g, hi);
-            tmem_st16x8u(t16 + kPfColP + 64 + 8 * g, lo);
+            float x0, x1;
+            f2_unpack(lt[y], x0, x1);
+            w.l += x0 + x1;
             if constexpr (PROBE) {
-              tmem_st16x8u(t16 + kPfColP + 32 + 8 * g, thi);
-              tmem_st16x8u(t16 + kPfColP + 96 + 8 * g, tlo);
+              f2_unpack(bt[y], x0, x1);
+              w.b += x0 + x1;
             }
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 8 * (jt & 1));
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          Row& w = y ? B : A;
-          float x0, x1;
-          f2_unpack(lt[y], x0, x1);
-          w.l += x0 + x1;
-          if constexpr (PROBE) {
-            f2_unpack(bt[y], x0, x1);
-            w.b += x0 + x1;
           }
         }
       }
