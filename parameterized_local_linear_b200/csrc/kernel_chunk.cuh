@@ -122,14 +122,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
   const uint32_t sQ = base + Geo::kOffQ, sR = base + Geo::kOffR;
   const uint32_t sK = base + Geo::kOffK, sV = base + Geo::kOffV;
   const uint32_t bar = base + Geo::kOffBar;
-  const uint32_t q_full = bar, k_full = bar + 16, k_empty = k_full + 8 * kSt,
-                 v_full = k_empty + 8 * kSt, v_ready = v_full + 8 * kSt,
-                 v_empty = v_ready + 8 * kSt;
-  // p_full: one per P buffer, since a warp may finish tile j + 1 before another
-  // finishes tile j
-  const uint32_t s_full = v_empty + 8 * kSt, s_free = s_full + 8, p_full = s_full + 16,
-                 o_done = s_full + 32, bar_drain = s_full + 40, red_full = s_full + 48;
-  constexpr int kOffMisc = Geo::kOffBar + 16 + 5 * 8 * kSt + 64;
+  // One per ring stage: K, V loaded; V converted; S and T written (which frees K);
+  // the value products done (which frees V). p_full: one per P buffer, since a
+  // warp may finish tile j + 1 before another finishes tile j.
+  const uint32_t k_full = bar, v_full = k_full + 8 * kSt, v_ready = v_full + 8 * kSt,
+                 s_full = v_ready + 8 * kSt, o_done = s_full + 8 * kSt;
+  const uint32_t s_free = o_done + 8 * kSt, p_full = s_free + 8, q_full = s_free + 24,
+                 bar_drain = s_free + 32, red_full = s_free + 40;
+  constexpr int kOffMisc = Geo::kOffBar + 5 * 8 * kSt + 48;
   // per stage, one word per 16 keys, written by the warp that converted them:
   // bit 0 the block is fp16, bit 1 the tile's page is in the pool
   int4* const v_info = reinterpret_cast<int4*>(gbase + kOffMisc);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   float* const red = reinterpret_cast<float*>(gbase + Geo::kOffRed);
   ChunkRange* const range_slot = reinterpret_cast<ChunkRange*>(gbase + kOffMisc + 20 * kSt + 16);
   static_assert(kOffMisc % 16 == 0 &&
-                    16 + 5 * 8 * kSt + 64 + 20 * kSt + 16 + sizeof(ChunkRange) <= 512,
+                    5 * 8 * kSt + 48 + 20 * kSt + 16 + sizeof(ChunkRange) <= 512,
                 "misc area");
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -148,16 +148,14 @@ __global__ void __launch_bounds__(kChThreads, 1)
     mbar_init(q_full, 1);
     for (int s = 0; s < kSt; ++s) {
       mbar_init(k_full + 8 * s, 1);
-      mbar_init(k_empty + 8 * s, 1);
       mbar_init(v_full + 8 * s, 1);
       mbar_init(v_ready + 8 * s, kChConvertWarps);
-      mbar_init(v_empty + 8 * s, 1);
+      mbar_init(s_full + 8 * s, 1);
+      mbar_init(o_done + 8 * s, 1);
     }
-    mbar_init(s_full, 1);
     mbar_init(s_free, kPfSoftmaxWarps);
     mbar_init(p_full, kPfSoftmaxWarps);
     mbar_init(p_full + 8, kPfSoftmaxWarps);
-    mbar_init(o_done, 1);
     mbar_init(bar_drain, 1);
     mbar_init(red_full, kPfSoftmaxWarps);
     *abort_flag = 0;
@@ -206,6 +204,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
   // Every role walks the same pieces and counts tiles over all of them: tile
   // jt uses ring stage jt % kSt in its (jt / kSt)-th round.
   const auto round_parity = [](int jt) { return (uint32_t)(jt / kSt) & 1u; };
+  const auto wait_round = [&](uint32_t bars, int jt) {
+    return mbar_wait_bounded(bars + 8 * (jt % kSt), round_parity(jt), p.timeout_ns, abort_flag);
+  };
 
   if (warp == 8) {
     // ------------------------------------------------- producer of K and V --
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (!in_pool) page = p.num_pages;  // out of range for the TMA too: reads zeros
         const int st = jt % kSt;
         const uint32_t ph = round_parity(jt);
-        ok = mbar_wait_bounded(k_empty + 8 * st, ph ^ 1, p.timeout_ns, abort_flag);
+        ok = jt < kSt || wait_round(s_full, jt - kSt);  // the stage's last K is read
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
         }
         __syncwarp();
-        ok = mbar_wait_bounded(v_empty + 8 * st, ph ^ 1, p.timeout_ns, abort_flag);
+        ok = jt < kSt || wait_round(o_done, jt - kSt);
         if (!__all_sync(0xffffffffu, ok)) {
           if (!(jt == 0 && skipped_k0))
             mbar_wait_bounded(k_full + 8 * st, ph, p.timeout_ns, nullptr);  // K in flight
@@ -354,10 +355,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
                            k + ko / 16, kIdescS, kk > 0, lead);
             }
           }
-          umma_commit_lead(s_full, lead);  // also frees the K stage: softmax warp 0 passes it on
+          umma_commit_lead(s_full + 8 * (jt % kSt), lead);
           ++jt;
         } else if (more) {
-          const bool done = mbar_wait_bounded(s_full, (jt - 1) & 1, p.timeout_ns, abort_flag);
+          const bool done = wait_round(s_full, jt - 1);
           if (!(ok = __all_sync(0xffffffffu, done) != 0)) break;
           load_queries(nx);
         }
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           const uint32_t fp16 = __shfl_sync(
               0xffffffffu, (vi.x & 1) | (vi.y & 1) << 1 | (vi.z & 1) << 2 | (vi.w & 1) << 3, 0);
           values(jv, fp16, j > pc.t0 + 1 ? 1u : 0u);
-          umma_commit_lead(o_done, lead);
+          umma_commit_lead(o_done + 8 * (jv % kSt), lead);
         }
       }
       pc = nx;
@@ -478,7 +479,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
     };
     bool ok = true;
     int jt = 0, np = 0;
-    int freed = 0;         // tiles whose V stage is passed back
     bool wide = false;     // the tile before filled both P buffers
     bool more = cur.next(p.sp, pc);
     while (ok && more) {
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       // few rows the others then have the schedulers for themselves.
       if ((quarter * 32 + half * 16) / p.G >= ntok) {
         for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
-          ok = mbar_wait_bounded(s_full, jt & 1, p.timeout_ns, abort_flag);
+          ok = wait_round(s_full, jt);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
           const int4 vi = v_info[st];
           const bool in_pool = (vi.x & 2) != 0;
           const bool f16 = (vi.x & vi.y & vi.z & vi.w & 1) != 0;
-          ok = ok && mbar_wait_bounded(s_full, jt & 1, p.timeout_ns, abort_flag);
+          ok = ok && wait_round(s_full, jt);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
@@ -526,12 +526,6 @@ __global__ void __launch_bounds__(kChThreads, 1)
           float sv[32], tv[32];
           tmem_ld16x64(t16 + kPfColS, sv);
           if constexpr (PROBE) tmem_ld16x64(t16 + kPfColT, tv);
-          // S_j, T_j complete: the score UMMAs have read K_j, and the value UMMAs
-          // of tile j - 2, issued before them, V and P of that tile
-          if (warp == 0 && lane == 0) {
-            mbar_arrive(k_empty + 8 * st);
-            for (; freed < jt - 1; ++freed) mbar_arrive(v_empty + 8 * (freed % kSt));
-          }
           tmem_wait_ld();
           tc_fence_before_sync();
           __syncwarp();
@@ -636,7 +630,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
             const bool wait = j > pc.t0 && (grow || wide || !f16);
             wide = !f16;
             if (!wait) return true;
-            const bool got = mbar_wait_bounded(o_done, (jt - 1) & 1, p.timeout_ns, abort_flag);
+            const bool got = wait_round(o_done, jt - 1);
             if (!__all_sync(0xffffffffu, got)) return false;
             tc_fence_after_sync();
             if (grow) {
@@ -742,15 +736,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(red_full);
       ok = mbar_wait_bounded(red_full, np & 1, p.timeout_ns, abort_flag) &&
-           mbar_wait_bounded(o_done, (jt - 1) & 1, p.timeout_ns, abort_flag);
+           wait_round(o_done, jt - 1);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       ++np;
       tc_fence_after_sync();
-      if (warp == 0 && lane == 0)
-        for (; freed < jt; ++freed) mbar_arrive(v_empty + 8 * (freed % kSt));
       const bool live = r_tok < ntok;
       const float lsum = rd[r], cs = rd[2 * kChunkRows + r] * 2048.f;
       // l and A carry 2^11; C and b, which carry 2^sigma, are brought to it
