@@ -432,7 +432,8 @@ int parallax_qk_norm_rope_backward(
     size_t workspace_bytes);
 
 /* Workspace bytes of parallax_qk_norm_rope_backward on the current device: the
- * status header and one [D] fp32 partial sum per block. 0 for bad arguments. */
+ * header (status word and counters, 0 between calls) and one [D] fp32 partial
+ * sum per block. 0 for bad arguments. */
 size_t parallax_qk_norm_rope_backward_workspace_bytes(int tokens, int Hq, int Hkv, int D);
 
 /*
@@ -444,15 +445,19 @@ size_t parallax_qk_norm_rope_backward_workspace_bytes(int tokens, int Hq, int Hk
  *    parallax_decode_paged (dtype for all; any page_size >= 1).
  *  - cu_seqlens_q [B + 1] int32, non-decreasing: sequence b's new tokens are
  *    rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1. NULL: one token per sequence
- *    (total_tokens = B). Rows outside cu_seqlens_q[0] .. cu_seqlens_q[B]-1 (a
- *    padded batch) are neither read nor written.
+ *    (total_tokens = B), and a row whose cache_seqlens is 0 is idle. Rows outside
+ *    cu_seqlens_q[0] .. cu_seqlens_q[B]-1 (a padded batch) and idle rows have
+ *    no output: their rows of q_out and r_out stay as they are.
  *  - cache_seqlens [B] int32: the sequences' lengths AFTER the append, as the
  *    attention call that follows takes them. With c new tokens, token j of a
  *    sequence becomes key cache_seqlens[b] - c + j. A key outside the block
  *    table or in a page outside the pool is not written and sets
  *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED. Two tokens with one slot (a page
  *    listed for two sequences): one of them is kept.
- *  - positions NULL: a token's position is its key index.
+ *  - positions NULL: a token's position is its key index (so that a key below 0,
+ *    of a sequence shorter than its new tokens, sets
+ *    PARALLAX_DEVICE_STATUS_POSITION_CLAMPED too).
+ *  - q_out may be q (r_out r) where the rows are contiguous; no other overlap.
  */
 int parallax_norm_rope_append(
     const void* q, const void* r, const void* k, const void* v, const void* q_weight,

@@ -518,11 +518,17 @@ def _call(name, args, stream):
     fn = getattr(_marshal_module or _marshal(), name)
     if stream is None:
         return fn(*args)
-    device = args[0].device
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_on(args[0].device, stream)):
         return fn(*args)
+
+
+def _stream_on(device, stream):
+    """A torch stream on `device` from a stream object or a handle."""
+    if not hasattr(stream, "cuda_stream"):
+        return torch.cuda.ExternalStream(int(stream), device=device)
+    if device.index not in (None, stream.device.index):
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return stream
 
 
 def _workspace_buffer(workspace):
@@ -566,11 +572,11 @@ def parallax_rope_table(max_positions: int, rotary_dim: int, base: float = 1e6, 
     fn = load_library().parallax_rope_table
     fn.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_double, ctypes.c_void_p]
     fn.restype = ctypes.c_int
-    out = torch.empty(max_positions, rotary_dim, dtype=torch.float32, device=device)
-    with torch.cuda.device(out.device):
-        if stream is not None:
-            out.record_stream(stream)
-        _check(fn(out.data_ptr(), max_positions, rotary_dim, float(base), _stream(stream)),
+    if stream is not None:
+        stream = _stream_on(torch.device(device), stream)
+    with torch.cuda.device(device), torch.cuda.stream(stream):  # (None: the current one)
+        out = torch.empty(max_positions, rotary_dim, dtype=torch.float32, device=device)
+        _check(fn(out.data_ptr(), max_positions, rotary_dim, float(base), _stream(None)),
                "parallax_rope_table")
     return out
 
@@ -613,9 +619,10 @@ def parallax_norm_rope_append(q, r, k, v, cos_sin, k_pages, v_pages, block_table
     returns (q, r) normed and rotated; k (likewise) and v go into the pools.
 
     cache_seqlens int32 [B]: the lengths after the append. cu_seqlens_q int32
-    [B + 1]: each sequence's rows, or None for one token per sequence; rows
-    past the last are left alone. positions int32 [tokens] or None (each
-    token's key index)."""
+    [B + 1]: each sequence's rows, or None for one token per sequence (of length
+    0: an idle row). Idle rows and rows past the last sequence have no output:
+    q_out and r_out keep what they hold there. positions int32 [tokens] or None
+    (each token's key index)."""
     return _call("norm_rope_append",
                  (q, r, k, v, cos_sin, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q,
                   positions, q_weight, r_weight, k_weight, eps, interleaved, q_out, r_out,

@@ -79,6 +79,7 @@ struct NormRopeParams {
   void* dx[3];
   long long dxs[3];
   float* partial;         // [blocks][D] sums of dz xh
+  unsigned int* done;     // [3] blocks of each kind whose partials are written
   float* dw[3];
 };
 
@@ -257,8 +258,9 @@ struct NrBatch {
   // caller sees it by the page it then lacks.
   __device__ long long key(const int32_t* cu, const int32_t* lens, int B, int t, int& b) const {
     if (cu == nullptr) {
-      b = t;
-      return (long long)__ldg(lens + t) - 1;
+      const int n = __ldg(lens + t);
+      b = n == 0 ? -1 : t;  // a length of 0: an idle row
+      return (long long)n - 1;
     }
     int last, n;
     if (B <= 32) {
@@ -321,6 +323,15 @@ struct NrRing {
     for (int st = 0; st < STAGES; ++st) mbar_init(bar(st), 1);
     mbar_fence_init();
   }
+  // Waits for a stage's copies. Where they do not land, reports it, gives the
+  // other stages' (parities as the ring's walk left them) as long and fails.
+  __device__ bool wait(int st, uint32_t parity, unsigned int* status) const {
+    if (mbar_wait_bounded(bar(st), parity, kNrTimeoutNs, nullptr)) return true;
+    atomicOr(status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
+    for (int s = 0; s < STAGES; ++s)
+      if (s != st) mbar_wait_bounded(bar(s), s > st ? parity : parity ^ 1, kNrTimeoutNs, nullptr);
+    return false;
+  }
 };
 
 // A unit of work is up to `rows` heads of one kind and token. A warp's units
@@ -337,7 +348,7 @@ struct NrUnits {
     t = per_token.quotient(unit);
     h0 = (unit - t * (int)per_token.d) * rows;
   }
-  __device__ void next() { unit = unit + stride < unit ? count : unit + stride; }
+  __device__ void next() { unit = count - unit > stride ? unit + stride : count; }
 };
 
 // 4 KB of rows per stage: 16 heads of 128 bf16 dimensions. Two blocks per SM.
@@ -447,10 +458,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   for (; at.valid(); at.next()) {
     int t, h0;
     at.place(t, h0);
-    if (!mbar_wait_bounded(ring.bar(st), parity, kNrTimeoutNs, nullptr)) {
-      atomicOr(p.status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
-      return;
-    }
+    if (!ring.wait(st, parity, p.status)) break;
     __syncwarp();  // the note
     const long long out_row = *ring.note(st);
     const int n = min(at.rows, H - h0);
@@ -506,7 +514,9 @@ __global__ void __launch_bounds__(kNrThreads, 2)
 }
 
 // Backward: dw stays in 16 registers per lane and is summed over the block's
-// rows in shared memory at the end, one [D] partial per block in a fixed order.
+// rows in shared memory at the end, one [D] partial per block in a fixed order,
+// and over the blocks by the last of them. (In a kernel of its own that sum took
+// 2 us more of a 777-token call.)
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kNrThreads, 2)
     parallax_norm_rope_backward_kernel(const NormRopeParams p) {
@@ -585,10 +595,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   for (; at.valid(); at.next()) {
     int t, h0;
     at.place(t, h0);
-    if (!mbar_wait_bounded(ring.bar(st), parity, kNrTimeoutNs, nullptr)) {
-      atomicOr(p.status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
-      return;
-    }
+    if (!ring.wait(st, parity, p.status)) break;
     const int n = min(at.rows, H - h0);
     const NrAngles ang = nr_angles<D, INTER, true>(ring.table(st), ln, p.rot);
     T* out = dx + (size_t)t * dxs + (size_t)(h0 + grp) * D;
@@ -642,7 +649,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     }
   }
   if (!norm) return;  // the whole block: one kind
-  __syncthreads();  // every copy has landed; the rings' space now holds the warps' sums
+  __syncthreads();  // no copy is in flight; the rings' space now holds the warps' sums
   float(*const red)[D] = reinterpret_cast<float(*)[D]>(ring_bytes);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -661,28 +668,33 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < kNrWarps; ++v) sum += red[v][d];
-    p.partial[(size_t)blockIdx.x * D + d] = sum;
+    __stcg(p.partial + (size_t)blockIdx.x * D + d, sum);
   }
-}
-
-// dw of each kind from its blocks' partials, in block order per thread.
-template <int D>
-__global__ void __launch_bounds__(1024) parallax_norm_rope_dw_kernel(const NormRopeParams p) {
-  constexpr int kParts = 1024 / D;
-  __shared__ float red[kParts][D];
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const int k = blockIdx.x, d = threadIdx.x % D, part = threadIdx.x / D;
-  if (p.H[k] == 0 || p.w[k] == nullptr) return;
-  float sum = 0.f;
-  for (int b = p.first_block[k] + part; b < p.first_block[k + 1]; b += kParts)
-    sum += __ldcg(p.partial + (size_t)b * D + d);
-  red[part][d] = sum;
+  // The kind's last block sums the partials, each thread and then the threads of
+  // a column in a fixed order. The counter wraps to 0 for the next call.
+  __shared__ bool last;
+  __threadfence();
   __syncthreads();
-  if (part == 0) {
+  if (threadIdx.x == 0) last = atomicInc(p.done + k, nblk - 1) == (unsigned)nblk - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  constexpr int kCols = D / 4, kParts = kNrThreads / kCols;
+  float4(*const sums)[kCols] = reinterpret_cast<float4(*)[kCols]>(ring_bytes);
+  const int c = threadIdx.x % kCols, part = threadIdx.x / kCols;
+  const float4* from = reinterpret_cast<const float4*>(p.partial) + (size_t)p.first_block[k] * kCols + c;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int b = part; b < nblk; b += kParts) {
+    const float4 v = __ldcg(from + (size_t)b * kCols);
+    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  }
+  sums[part][c] = s;
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += kNrThreads) {
     float all = 0.f;
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) all += red[i][d];
+    for (int i = 0; i < kParts; ++i) all += reinterpret_cast<const float*>(sums[i])[d];
     p.dw[k][d] = all;
   }
 }

@@ -84,6 +84,7 @@ void deal_blocks(NormRopeParams& p, int kinds, int most, int D, int stage_rows, 
 constexpr int kNrForwardBlocksPerSm = 2;
 constexpr double kNrForwardUnitCost = 1.5;
 constexpr int kNrBackwardBlocksPerSm = 2;
+constexpr int kNrDoneWord = 8;  // of the workspace header: counters that are 0 between calls
 
 template <typename T, int D, bool INTER, bool APPEND>
 int launch_forward(NormRopeParams& p, cudaStream_t s) {
@@ -125,10 +126,7 @@ int launch_backward(const NormRopeParams& p, cudaStream_t s) {
   constexpr int kSmem = NrBackwardRing::kSmem;
   int st = set_smem_once(kernel, kSmem, done);
   if (st != PARALLAX_OK) return st;
-  st = launch_pdl(kernel, dim3((unsigned)p.first_block[3]), kNrThreads, kSmem, s, p);
-  if (st != PARALLAX_OK) return st;
-  if (!p.w[0] && !p.w[1] && !p.w[2]) return PARALLAX_OK;
-  return launch_pdl(parallax_norm_rope_dw_kernel<D>, dim3(3), 1024, 0, s, p);
+  return launch_pdl(kernel, dim3((unsigned)p.first_block[3]), kNrThreads, kSmem, s, p);
 }
 
 template <typename T>
@@ -252,6 +250,7 @@ extern "C" int parallax_qk_norm_rope_backward(
   deal_blocks(p, 3, kNrBackwardBlocksPerSm * sm, D,
               NrBackwardRing::kBytes / (D * (int)elem_size(dtype)), 0.0);
   p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);
+  p.done = p.status + kNrDoneWord;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dtype == PARALLAX_DTYPE_BF16 ? dispatch_backward<__nv_bfloat16>(p, D, interleaved != 0, s)
                                       : dispatch_backward<float>(p, D, interleaved != 0, s);

@@ -313,6 +313,57 @@ def test_append_positions_without_probe_and_bad_slots():
         assert int(ws[:4].view(torch.int32)) == 2
 
 
+def test_append_idle_rows_in_place_and_default_positions():
+    """One token per sequence, two of them idle (length 0): no output, no slot,
+    no status. q and r are their own outputs."""
+    Hq, Hkv, D, ps = 8, 2, 128, 16
+    seqs = [(1, 5), (1, 0), (1, 33), (1, 0), (1, 16)]
+    kp, vp, table, _, lens = make_cache(seqs, ps, Hkv, D, torch.bfloat16, seed=52)
+    (q, r, k, v), w, _, cs = inputs(5, Hq, Hkv, D, D, torch.bfloat16, seed=53, fused=False)
+    live = torch.tensor([0, 2, 4], device="cuda")
+    pos = (lens - 1).clamp(min=0)
+    fq, fr, fk = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w)
+    want_q, want_r, want_k, want_v = q.clone(), r.clone(), kp.clone(), vp.clone()
+    want_q[live], want_r[live] = fq[live], fr[live]
+    for b in live.tolist():
+        page, at = int(table[b, int(pos[b]) // ps]), int(pos[b]) % ps
+        want_k[page, at], want_v[page, at] = fk[b], v[b]
+    ws = pl.status_workspace("cuda")
+    qo, ro = pl.parallax_norm_rope_append(q, r, k, v, cs, kp, vp, table, lens, None, None, *w,
+                                          q_out=q, r_out=r, workspace=ws)
+    assert qo.data_ptr() == q.data_ptr()
+    for got, want in ((q, want_q), (r, want_r), (kp, want_k), (vp, want_v)):
+        assert torch.equal(got, want)
+    assert int(ws[:4].view(torch.int32)) == 0
+
+
+def test_backward_calls_sharing_a_workspace():
+    """Calls of other sizes, head sizes and weights one after the other on one
+    workspace: the block counters are 0 again after each."""
+    sizes = [(1, 1, 1, 64), (700, 16, 8, 128), (3, 6, 2, 64), (700, 16, 8, 128), (90, 16, 16, 128)]
+    nbytes = max(pl.norm_rope_backward_workspace(*s, "cuda").numel() for s in sizes)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    for j, (n, Hq, Hkv, D) in enumerate(sizes):
+        (q, r, k, _), w, pos, cs = inputs(n, Hq, Hkv, D, D, torch.float32, seed=54 + j)
+        if j == 4:
+            w[1] = None
+        dy = [x.contiguous() for x in (r, q, k)]
+        want = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w)
+        got = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w, workspace=ws)
+        for a, b in zip(want, got):
+            assert (a is None and b is None) or torch.equal(a, b)
+    assert not ws[:256].any()
+
+
+def test_table_on_a_stream():
+    want = pl.parallax_rope_table(500, 64, 1e4)
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        got = pl.parallax_rope_table(500, 64, 1e4, stream=stream)
+        s.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_streams_graphs_and_devices_context():
     """On another stream, and captured twice with separate workspaces."""
     (q, r, k, _), w, pos, cs = inputs(300, 8, 4, 128, 128, torch.bfloat16, seed=60)

@@ -145,3 +145,16 @@ def test_binding_needs_cuda_tensors():
         pl.parallax_qk_norm_rope(x, None, x, x)
     with pytest.raises(ValueError):
         pl.parallax_prefill_paged(x, None, x, x, x, x)
+
+
+def test_stream_of_another_device_is_refused():
+    class Fake:
+        def __init__(self, device):
+            self.device, self.cuda_stream = torch.device(device), 0
+
+    with pytest.raises(ValueError):
+        pl._call("prefill_paged", (Fake("cuda:0"),), Fake("cuda:1"))
+    with pytest.raises(ValueError):
+        pl.parallax_rope_table(16, 64, device="cuda:0", stream=Fake("cuda:1"))
+    s = Fake("cuda:1")
+    assert pl._stream_on(torch.device("cuda:1"), s) is s
