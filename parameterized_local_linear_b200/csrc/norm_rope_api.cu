@@ -82,7 +82,7 @@ void deal_blocks(NormRopeParams& p, int kinds, int most, int D, int stage_rows, 
 }
 
 constexpr int kNrForwardBlocksPerSm = 2;
-constexpr double kNrForwardUnitCost = 1.5;
+constexpr double kNrForwardUnitCost = 1.5;  // (the backward's steps are longer: 0)
 constexpr int kNrBackwardBlocksPerSm = 2;
 constexpr int kNrDoneWord = 8;  // of the workspace header: counters that are 0 between calls
 
