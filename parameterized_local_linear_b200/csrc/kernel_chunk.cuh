@@ -36,13 +36,25 @@
 //    rounded to 17 bits and enter as exact bf16 hi + lo pairs. A UMMA takes 16
 //    keys, so each takes the form of its block.
 //
+// What bounds it. A 128 x 64 tile of D = 128 is 8.4 MFLOP of useful work and, at
+// the rates measured for these UMMAs one by one (S, T: 50 cycles per 16 dims, fed
+// from shared memory; value products: 65 per 16 keys), 1320 cycles of tensor
+// pipe. Observed 2000: each scheduler has two softmax warps, and one's chain
+// (TMEM load, mask, maximum, 2^x, conversion, TMEM store, barrier) takes 2600
+// cycles for a tile, half hidden by the other's. Measured, 16 query on 8 kv heads
+// of 128: 2048 rows over 32768 keys 1050 us (1.0 PFLOP/s) at full clock, 1200
+// when the power limit holds the clock at 1.5 GHz; 512 rows over 8192 keys 79 us;
+// 4 drafted tokens of 32 sequences of 4096 keys 121 us (4.4 TB/s).
+//
 // Slots past a sequence's length may hold anything (NaN too): their scores are
 // masked before use, and the converting warps zero their V rows, which weight 0
 // would not remove.
 //
-// Warps 0-7 softmax (two threads per row), 8 producer, 9 UMMA issuer, 10-11 V.
-// TMEM columns as in the prefill kernel: S [0,64) T [64,128) P [128,256) O_A
-// [256,256+D) O_C [256+D,256+2D). Every wait is bounded.
+// Warps 0-7 softmax (16 rows each, four threads for rows ra and ra + 8), 8
+// producer, 9 UMMA issuer, 10-11 V. TMEM columns as in the prefill kernel: S
+// [0,64) T [64,128) P [128,256), two buffers of fp16 weights (e, then e s, 32
+// columns each) or one of hi + lo pairs, O_A [256,256+D) O_C [256+D,256+2D).
+// Every wait is bounded.
 #pragma once
 
 #include "chunk_partition.cuh"
@@ -88,7 +100,7 @@ struct ChGeom {
   static constexpr int kKVBytes = kH * kChunkKeys * 128;  // K (or V) tile
   static constexpr int kOffQ = 0, kOffR = kQBytes, kOffK = 2 * kQBytes;
   static constexpr int kOffV = kOffK + kStages * kKVBytes;
-  static constexpr int kOffRed = kOffV + kStages * kKVBytes;  // l, b of both key halves
+  static constexpr int kOffRed = kOffV + kStages * kKVBytes;  // l, b, 2^-sigma, m of each row
   static constexpr int kOffBar = kOffRed + 2 * 4 * kChunkRows * 4;  // two pieces' worth
   static constexpr int kSmem = kOffBar + 512 + 1024;  // barriers, flags, alignment
   static constexpr uint32_t kColOA = 256, kColOC = 256 + D;
@@ -219,11 +231,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
       for (int j = pc.t0; j < pc.t1; ++j, ++jt) {
         const int k0 = j * kChunkKeys, w = (j - pc.t0) & 31;
         if (w == 0) {  // the page ids of the next 32 tiles, one per lane
-          const int kl = (j + lane) * kChunkKeys;
+          // (none past the piece's tiles, whose key index need not fit an int)
+          const int kl = j + lane < pc.t1 ? (j + lane) * kChunkKeys : pc.s.n;
           ids = kl < pc.s.n ? __ldg(row + kl / p.page_size) : -1;
           // a page id outside the pool: its keys are left out
-          if (j + lane < pc.t1 && kl < pc.s.n && (ids < 0 || ids >= p.num_pages))
-            atomicOr(p.status, 2u);
+          if (kl < pc.s.n && (ids < 0 || ids >= p.num_pages)) atomicOr(p.status, 2u);
         }
         int page = __shfl_sync(0xffffffffu, ids, w);
         const bool in_pool = page >= 0 && page < p.num_pages;
@@ -623,9 +635,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
           if (grow) update(ma, mb, sa, sb);  // (the row's four threads need a common value)
           factors();
           if (f16) weights();
-          // A tile of fp16 blocks alternates between two P buffers, and its buffer
-          // is free (above). One with hi + lo weights fills both. O may need a
-          // rescale. For either, the products of the tile before must be done.
+          // Tiles of fp16 blocks alternate between two P buffers, and this one's is
+          // free: the value products of tile jt - 2 were issued before the scores
+          // of jt, whose commit (s_full) covers them. A tile with hi + lo weights
+          // fills both buffers, and O may need a rescale: for either, the products
+          // of the tile before must be done.
           const auto prev_done_and_rescale = [&]() -> bool {
             const bool wait = j > pc.t0 && (grow || wide || !f16);
             wide = !f16;
@@ -811,6 +825,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
 // the columns (kChunkMergeCols float4 columns of A and of C) of the item that
 // ends in range c, one row per thread, the records in order:
 //   M = max_j m_j, w_j = 2^(m_j - M), sums of w_j (l_j, b_j, A_j, C_j).
+// Latency: 3 to 4 us behind the attention kernel. 16 (D = 128) slices per item
+// rather than one block, so that a few items use many SMs.
 constexpr int kChunkMergeCols = 2;
 
 template <int D, bool PROBE>

@@ -149,3 +149,68 @@ def test_oracle_chunk_rows_are_decode_rows():
                 want = oracle.parallax_decode_paged(q[row:row + 1], r[row:row + 1], kp, vp,
                                                     table[b:b + 1], np.array([keys]), 0.1)
                 np.testing.assert_allclose(got[row:row + 1], want, rtol=1e-9, atol=1e-12)
+
+
+def ceil_sum(a, T, m):
+    """chunk_ceil_sum of csrc/chunk_partition.cuh."""
+    period = (1 if T % KEYS == 0 else KEYS) if T >= KEYS else (KEYS // T if KEYS % T == 0 else KEYS)
+    rise = period * T // KEYS
+    u, v = divmod(m, period)
+    total = 0
+    for i in range(1, min(m, period) + 1):
+        first = (a + i * T + KEYS - 1) // KEYS
+        terms = u + (1 if i <= v else 0)
+        total += terms * first + rise * (terms * (terms - 1) // 2)
+    return total
+
+
+@pytest.mark.parametrize("G", range(1, 129))
+def test_the_closed_sum_is_the_sum_of_the_tiles(G):
+    """Every row tile height, chunks of any offset and of up to 300 row tiles."""
+    rnd, T = random.Random(G), ROWS // G
+    for a in (0, 1, 63, 64, rnd.randint(0, 10 ** 6)):
+        want = 0
+        for m in range(300):
+            assert ceil_sum(a, T, m) == want, (a, T, m)
+            want += -(-(a + (m + 1) * T) // KEYS)
+
+
+def search32(below, count):
+    """The largest i with below(i) (below(0) holds), 32 candidates a step, as
+    chunk_locate and NrBatch::search do it; counts the steps."""
+    lo, hi, steps = 0, count, 0
+    while hi - lo > 1:
+        step = (hi - lo + 31) // 32
+        votes = [lo + (x + 1) * step < hi and below(lo + (x + 1) * step) for x in range(32)]
+        k = min((x for x in range(31) if not votes[x]), default=31)
+        lo += k * step
+        hi = min(hi, lo + step)
+        steps += 1
+    return lo, steps
+
+
+def test_the_32_way_search_finds_every_place():
+    for count in list(range(1, 200)) + [1023, 1024, 1025, 32769, 10 ** 6]:
+        for at in {0, 1, 30, 31, 32, 33, count // 2, count - 2, count - 1} & set(range(count)):
+            got, steps = search32(lambda i: i <= at, count)
+            assert got == at and steps <= 5
+    rnd = random.Random(0)  # no order among the votes: it still ends, in range
+    for _ in range(200):
+        got, steps = search32(lambda i: rnd.random() < 0.5, rnd.randint(1, 5000))
+        assert 0 <= got < 5000 and steps <= 5
+
+
+def test_the_divisor_is_exact():
+    """NrDivisor: quotients of 31-bit numbers by a multiplication."""
+    rnd = random.Random(1)
+    for d in list(range(1, 300)) + [2 ** k + e for k in range(8, 31) for e in (-1, 0, 1)] + [2 ** 31 - 1]:
+        s = 0
+        while 2 ** s < d:
+            s += 1
+        m = (((2 ** s - d) << 32) // d + 1) & 0xffffffff
+        for n in [0, 1, d - 1, d, d + 1, 2 ** 31 - 1] + [rnd.randrange(2 ** 31) for _ in range(50)] + \
+                 [x * d + e for x in (rnd.randrange(2 ** 31 // d) for _ in range(10)) for e in (-1, 0)]:
+            if 0 <= n < 2 ** 31:
+                # (the sum mulhi + n stays below 2^32 for these n)
+                assert ((m * n) >> 32) + n < 2 ** 32
+                assert (((m * n) >> 32) + n) >> s == n // d, (n, d)

@@ -234,6 +234,59 @@ def test_malformed_cu_seqlens_stays_in_bounds():
     assert int(ws[:4].view(torch.int32)) == 2 and got.isfinite().all()
 
 
+def test_many_ragged_sequences():
+    """More sequences than a warp's lanes, some without new tokens, chunks that
+    end anywhere in their row tiles."""
+    g = torch.Generator().manual_seed(0)
+    q = (torch.randint(0, 40, (150,), generator=g) * (torch.rand(150, generator=g) < 0.7)).tolist()
+    seqs = [(c, c + int(x)) for c, x in zip(q, torch.randint(0, 300, (150,), generator=g))]
+    for causal in (True, False):
+        q, r, kp, vp, table, cu, lens = make(seqs, 64, 6, 2, 64, 112)
+        got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, causal=causal)
+        o, S = reference(q, r, kp, vp, table, cu, lens, causal, 64 ** -0.5)
+        check(got, o, S, 340, causal)
+
+
+def test_shared_pages_and_two_calls_at_once():
+    """Two sequences that share their first pages, in two calls on two streams
+    with a workspace each."""
+    seqs = [(40, 200), (7, 150)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 8, 4, 128, 113, poison=False)
+    table[1, :2] = table[0, :2]
+    o, S = reference(q, r, kp, vp, table, cu, lens, True, 128 ** -0.5)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ws = [pl.prefill_paged_workspace(2, 47, 8, 4, 128, q.device) for _ in streams]
+    outs = [torch.zeros_like(q) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, w, out in zip(streams, ws, outs):
+            pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, out=out, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    check(outs[0], o, S, 200)
+    assert torch.equal(*outs)
+
+
+def test_pools_past_32_bit_offsets():
+    """Keys in pages whose offsets pass 2^31 elements (2^32 bytes) of the pools, and
+    the same pages first in a small pool: the append and the attention give the same."""
+    Hq, Hkv, D, ps, pages = 4, 2, 128, 64, 140000
+    assert (pages - 8) * ps * Hkv * D > 2 ** 31
+    (q, r, k, v), w, _, cs = rope_inputs(300, Hq, Hkv, D, D, torch.bfloat16, 114)
+    cu = torch.tensor([0, 170, 300], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([170, 130], dtype=torch.int32, device="cuda")
+    small = torch.tensor([[5, 1, 7], [0, 3, 2]], dtype=torch.int32, device="cuda")
+    got = []
+    for n, table in ((8, small), (pages, small + pages - 8)):
+        kp, vp = (torch.empty(n, ps, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        kp[-8:], vp[-8:] = 0, 0
+        a, b = pl.parallax_norm_rope_append(q, r, k, v, cs, kp, vp, table, lens, cu, None, *w)
+        out = pl.parallax_prefill_paged(a, b, kp, vp, table, lens, cu)
+        got.append((a, b, kp[-8:].clone(), vp[-8:].clone(), out))
+        del kp, vp
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert got[0][4].abs().sum() > 0
+
+
 def test_one_token_form_is_the_decode():
     seqs = [(1, 300), (1, 1), (1, 64), (1, 129)]
     q, r, kp, vp, table, cu, lens = make(seqs, 64, 16, 8, 128, 99, poison=False)
