@@ -39,9 +39,11 @@
 // What bounds it. A 128 x 64 tile of D = 128 is 8.4 MFLOP of useful work and, at
 // the rates measured for these UMMAs one by one (S, T: 50 cycles per 16 dims, fed
 // from shared memory; value products: 65 per 16 keys), 1320 cycles of tensor
-// pipe. Observed 2000: each scheduler has two softmax warps, and one's chain
-// (TMEM load, mask, maximum, 2^x, conversion, TMEM store, barrier) takes 2600
-// cycles for a tile, half hidden by the other's. Measured, 16 query on 8 kv heads
+// pipe. Observed 2000: the issuer's loop (its 24 UMMAs and two waits), a softmax
+// warp's chain (TMEM load, mask, maximum, 2^x, conversion, TMEM store, barrier:
+// 2600 cycles, two warps per scheduler) and the V conversion (two warps) are each
+// near that. More softmax or converting warps leave too few registers (alternate
+// tiles to two sets of eight warps: 15% slower). Measured, 16 query on 8 kv heads
 // of 128: 2048 rows over 32768 keys 1050 us (1.0 PFLOP/s) at full clock, 1200
 // when the power limit holds the clock at 1.5 GHz; 512 rows over 8192 keys 79 us;
 // 4 drafted tokens of 32 sequences of 4096 keys 121 us (4.4 TB/s).
