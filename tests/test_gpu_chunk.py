@@ -322,6 +322,53 @@ def test_streams_and_two_graphs():
     assert all(torch.equal(want, out) for _, out, _ in graphs)
 
 
+def test_a_batch_without_new_tokens_is_left_alone():
+    q, r, kp, vp, table, _, lens = make([(3, 70), (2, 9)], 64, 4, 2, 128, 115, poison=False)
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 5.0)
+    ws = pl.prefill_paged_workspace(2, 5, 4, 2, 128, q.device)
+    pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, out=out, workspace=ws)
+    assert (out == 5).all() and int(ws[:4].view(torch.int32)) == 0
+
+
+def test_a_captured_step_follows_its_lengths():
+    """Norm, append and attention of a padded batch in one graph, replayed for
+    chunks and lengths that change in place."""
+    Hq, Hkv, D, ps, B, n = 8, 4, 128, 64, 3, 90
+    kp, vp = torch.zeros(2, 16, ps, Hkv, D, device="cuda").bfloat16().unbind(0)
+    (q, r, k, v), w, _, cs = rope_inputs(n, Hq, Hkv, D, D, torch.bfloat16, 116)
+    table = torch.arange(15, dtype=torch.int32, device="cuda").view(3, 5).clone()
+    cu = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    ws = pl.prefill_paged_workspace(B, n, Hq, Hkv, D, q.device)
+    a, b, out = (torch.zeros(n, Hq, D, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+
+    def step(kp, vp, a, b, out, ws):
+        pl.parallax_norm_rope_append(q, r, k, v, cs, kp, vp, table, lens, cu, None, *w, q_out=a,
+                                     r_out=b, workspace=ws)
+        pl.parallax_prefill_paged(a, b, kp, vp, table, lens, cu, out=out, workspace=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(kp, vp, a, b, out, ws)
+    kp2, vp2, a2, b2, out2, ws2 = (x.clone() for x in (kp, vp, a, b, out, ws))
+    done = torch.zeros(B, dtype=torch.int32)
+    for chunks in ([40, 30, 20], [1, 0, 70], [1, 1, 1], [0, 85, 5]):
+        c = torch.tensor(chunks, dtype=torch.int32)
+        done += c
+        cu[1:].copy_(c.cumsum(0).int())
+        lens.copy_(done)
+        q.copy_(q.roll(7, 0)), r.copy_(r.roll(7, 0)), k.copy_(k.roll(7, 0)), v.copy_(v.roll(7, 0))
+        graph.replay()
+        step(kp2, vp2, a2, b2, out2, ws2)
+        m = int(c.sum())
+        for x, y in ((kp, kp2), (vp, vp2), (a, a2), (b, b2), (out, out2)):
+            assert torch.equal(x, y)
+        o, S = reference(a, b, kp, vp, table, cu, lens, True, D ** -0.5)
+        check(out[:m], o[:m], S[:m], 200, chunks)
+    assert int(ws[:4].view(torch.int32)) == 0
+
+
 def test_bounded_wait_reports_and_context_survives():
     """The producer never loads the first K tile: the waits run out, the status
     word says so, and the next call is right."""

@@ -134,6 +134,33 @@ def test_nonfinite_values_stay_in_their_row():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 elements of q: the last tokens are those of a small call, in
+    the packed and in the batched layout, forward and backward."""
+    n, Hq, Hkv, D = 1_050_000, 16, 1, 128
+    assert n * Hq * D > 2 ** 31
+    q = torch.zeros(n, Hq, D, device="cuda", dtype=torch.bfloat16)
+    k = torch.zeros(n, Hkv, D, device="cuda", dtype=torch.bfloat16)
+    m = 50
+    (sq, _, sk, _), w, _, cs = inputs(m, Hq, Hkv, D, D, torch.bfloat16, seed=70)
+    q[-m:], k[-m:] = sq, sk
+    pos = torch.zeros(n, device="cuda", dtype=torch.int32)
+    pos[-m:] = torch.arange(m, device="cuda", dtype=torch.int32)
+    args = (w[0], None, w[2])
+    want = pl.parallax_qk_norm_rope(sq, None, sk, cs, pos[-m:], *args)
+    got = pl.parallax_qk_norm_rope(q, None, k, cs, pos, *args)
+    assert torch.equal(got[0][-m:], want[0]) and torch.equal(got[2][-m:], want[2])
+    assert not got[0][:-m].any()
+    wantg = pl.parallax_qk_norm_rope_backward(want[0], None, want[2], sq, None, sk, cs, pos[-m:], *args)
+    gotg = pl.parallax_qk_norm_rope_backward(*got, q, None, k, cs, pos, *args)
+    assert torch.equal(gotg[0][-m:], wantg[0]) and torch.equal(gotg[2][-m:], wantg[2])
+    del got, gotg
+    L = n // 2
+    y = pl.parallax_qk_norm_rope(q, None, k, cs, pos, *args, seq_len=L)
+    assert torch.equal(y[0][1, :, -m:].transpose(0, 1), want[0])
+    assert torch.equal(y[2][1, :, -m:].transpose(0, 1), want[2])
+
+
 def test_zero_rows_and_position_clamp():
     (q, r, k, _), w, pos, cs = inputs(6, 4, 2, 64, 64, torch.float32, seed=5, npos=100)
     q.zero_()
