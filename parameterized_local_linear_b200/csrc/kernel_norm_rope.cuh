@@ -330,7 +330,8 @@ struct NrRing {
   // Waits for a stage's copies. Where they do not land, reports it, gives the
   // other stages' (parities as the ring's walk left them) as long and fails.
   __device__ bool wait(int st, uint32_t parity, unsigned int* status) const {
-    if (mbar_wait_bounded(bar(st), parity, kNrTimeoutNs, nullptr)) return true;
+    const bool got = mbar_wait_bounded(bar(st), parity, kNrTimeoutNs, nullptr);
+    if (__all_sync(0xffffffffu, got)) return true;  // (the warp goes on or gives up as one)
     atomicOr(status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
     for (int s = 0; s < STAGES; ++s)
       if (s != st) mbar_wait_bounded(bar(s), s > st ? parity : parity ^ 1, kNrTimeoutNs, nullptr);
@@ -453,6 +454,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   };
 #pragma unroll 1
   for (int st = 0; st < kSt; ++st) load(st);
+  __syncwarp();  // the notes (later ones: the barrier that frees each stage)
 
   f32x2 wa[4], wb[4];
   const bool norm = wt != nullptr;
@@ -468,7 +470,6 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     int t, h0;
     at.place(t, h0);
     if (!ring.wait(st, parity, p.status)) break;
-    __syncwarp();  // the note
     const long long out_row = *ring.note(st);
     const int n = min(at.rows, H - h0);
     if (out_row >= 0) {
