@@ -45,8 +45,8 @@ def _build_marshal() -> None:
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
          "-I", sysconfig.get_paths()["include"], "-I", inc,
          "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, "-I", INCLUDE,
-         "-o", MARSHAL + ".tmp", MARSHAL_SOURCE, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
-         "-ltorch_python", "-L", PKG, "-l:libparallax.so", "-Wl,-rpath,$ORIGIN"], check=True)
+         "-o", MARSHAL + ".tmp", MARSHAL_SOURCE, "-L", lib, "-lc10", "-lc10_cuda",
+         "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L", PKG, "-l:libparallax.so", "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(MARSHAL + ".tmp", MARSHAL)
 
 

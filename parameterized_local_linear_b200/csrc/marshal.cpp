@@ -7,8 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -102,9 +101,14 @@ struct Call {
     if (t) dense(*t, name, shape, at::kInt);
     return static_cast<const int32_t*>(ptr(t));
   }
+  // A new tensor on q's device, from the allocator without the dispatcher (a call
+  // makes up to seven, 0.25 us less each).
+  Tensor fresh(at::IntArrayRef shape, at::ScalarType type) const {
+    return Tensor(at::detail::empty_cuda(shape, type, q.device(), std::nullopt));
+  }
   Tensor output(PyObject* o, const char* name, at::IntArrayRef shape) const {
     const Tensor* t = tensor_or_none(o, name);
-    if (!t) return at::empty(shape, q.options());
+    if (!t) return fresh(shape, q.scalar_type());
     dense(*t, name, shape, q.scalar_type());
     return *t;
   }
@@ -116,7 +120,7 @@ struct Call {
       return *t;
     }
     if (bytes == 0) bad("invalid arguments for a workspace size");
-    Tensor t = at::empty({(int64_t)bytes}, q.options().dtype(at::kByte));
+    Tensor t = fresh({(int64_t)bytes}, at::kByte);
     t.narrow(0, 0, 256).zero_();
     return t;
   }
@@ -226,14 +230,14 @@ PyObject* qk_norm_rope_backward(PyObject* const* a) {
   const Out3 out(b[11]);
   const auto grad = [&](PyObject* o, const char* name, int H) {
     const Tensor* t = tensor_or_none(o, name);
-    return t ? *t : at::empty({x.n, H, x.D}, x.c.q.options());
+    return t ? *t : x.c.fresh({x.n, H, x.D}, type);
   };
   const Tensor dq = grad(out.at[0], "out[0]", x.Hq), dk = grad(out.at[2], "out[2]", x.Hkv);
   const Tensor dr = x.r ? grad(out.at[1], "out[1]", x.Hq) : Tensor();
   const long long tq = x.c.rows(dq, "out[0]", x.Hq), tk = x.c.rows(dk, "out[2]", x.Hkv);
   const long long tr = x.r ? x.c.rows(dr, "out[1]", x.Hq) : 0;
   const auto dweight = [&](void* w) {
-    return w ? at::empty({x.D}, x.c.q.options().dtype(at::kFloat)) : Tensor();
+    return w ? x.c.fresh({x.D}, at::kFloat) : Tensor();
   };
   const Tensor dqw = dweight(x.qw), drw = dweight(x.rw), dkw = dweight(x.kw);
   const auto fp = [](const Tensor& t) {
@@ -325,7 +329,7 @@ PyObject* prefill_paged(PyObject* const* a) {
   const Pool pool(c, a[2], a[3], a[4], len.B, Hkv);
   Tensor out;
   if (a[10] == Py_None && len.cu)  // rows past the last sequence are not written
-    out = at::zeros(c.q.sizes(), c.q.options());
+    out = c.fresh(c.q.sizes(), at::kBFloat16).zero_();
   else
     out = c.output(a[10], "out", c.q.sizes());
   const Tensor ws = c.workspace(
