@@ -488,7 +488,11 @@ int parallax_norm_rope_append(
  *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED, as does a causal sequence with
  *    more new tokens than keys.
  *  - Slots past a sequence's length may hold anything. Keys and values below
- *    it must be finite: a row's tiles include keys behind the row's position.
+ *    it must be finite (values below 2^60 in magnitude): a row's tiles include
+ *    keys behind the row's position. Values enter the products with all their
+ *    bits; the weights e and e*s as one fp16 term each (11 bits), or as bf16
+ *    hi + lo pairs (17 bits) for 16 keys one of whose values is not 0 and not
+ *    in [2^-25, 2^8) in magnitude.
  *  - A page id outside [0, num_pages) is not read: its keys are left out and
  *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED is set.
  *  - probe != 0: the Parallax output (r required); probe == 0: softmax.

@@ -30,11 +30,14 @@
 //  - e s 2^sigma: sigma is a power of two per row, set by the row's largest |s|
 //    so far (|s| 2^sigma below 2^11) and lowered with O_C and b when it grows,
 //    as O_A and l are when the maximum does.
-//  - V: a block of 16 keys whose largest |v| is 0 or in [2^-8, 2^16) becomes
-//    fp16: exact down to 2^-17, within 2^-25 below. Any other block (far
-//    values, tiny ones, infinities) stays bf16, and its keys' weights are
-//    rounded to 17 bits and enter as exact bf16 hi + lo pairs. A UMMA takes 16
-//    keys, so each takes the form of its block.
+//  - V: a block of 16 keys whose values are all 0 or of magnitude [2^-25, 2^8)
+//    becomes fp16, times 2^8, which is exact for every one of them (8 significant
+//    bits; fp16's last step is 2^-24). Any other block (far values, tiny ones,
+//    infinities) stays bf16, and its keys' weights are rounded to 17 bits and
+//    enter, times 2^8 too, as exact bf16 hi + lo pairs. A UMMA takes 16 keys, so
+//    each takes the form of its block. (Looking only at a block's largest value
+//    costs 4 drafted tokens 119 us instead of 131 and 512 rows 79 instead of 82,
+//    but loses the bits of a dimension that is small in every key.)
 //
 // What bounds it. A 128 x 64 tile of D = 128 is 8.4 MFLOP of useful work and, at
 // the rates measured for these UMMAs one by one (S, T: 50 cycles per 16 dims, fed
@@ -70,6 +73,9 @@ namespace plx {
 // instead of two left 128, and the softmax spilled)
 constexpr int kChThreads = 384;
 constexpr int kChConvertWarps = 2;
+// fp16 values carry 2^kChValueShift, and so O_A and O_C
+constexpr int kChValueShift = 8;
+constexpr float kChValueScale = 1 << kChValueShift;
 
 // What the merge kernel does for one CTA: the item that ends in its range after
 // tiles in earlier ones. Written by the attention kernel, so that the merge
@@ -402,6 +408,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
   } else if (warp >= 10) {
     // ------------------------------- V: bf16 to fp16, rows past the end to 0 --
     constexpr int kWords = Geo::kH * 16 * 8 / 32;  // 16-byte words per lane
+    // bf16 bits of 2^8, of 2^-25 and of 2^-22 (from there fp16 is normal); what
+    // multiplies a pair of values below 2^8 by 2^8 (a 0 becomes 2^-119, 0 in fp16)
+    constexpr uint32_t kBelow = (127 + 16 - kChValueShift) << 7,
+                       kFrom = (127 - 17 - kChValueShift) << 7,
+                       kNormal = (127 - 14 - kChValueShift) << 7, kPair = 0x00010001u,
+                       kTimes = kPair * (kChValueShift << 7),
+                       kMove = kPair * (((15 - 127 + kChValueShift) & 31) << 10);
+    // Per half: max(far, 2 (|v| - kNormal)) of unsigned 16 bits, so that values below
+    // kNormal wrap to far ones. (v + v drops the signs; the low half's goes into the
+    // last bit of the high half, where it changes no comparison with an even bound.)
+    const auto range_max = [](uint32_t far, uint32_t v) {
+      return __viaddmax_u16x2(v + v, kPair * (0x10000u - 2 * kNormal), far);
+    };
     bool ok = true;
     int jt = 0;
     while (ok && cur.next(p.sp, pc)) {
@@ -434,30 +453,57 @@ __global__ void __launch_bounds__(kChThreads, 1)
               if ((warp - 10 + kChConvertWarps * y) * 16 + (i % 4) * 4 + lane / 8 >= left)
                 x[y][i] = make_uint4(0, 0, 0, 0);
         }
-        bool f16[kBlocks];
+        bool f16[kBlocks], direct[kBlocks];
 #pragma unroll
         for (int y = 0; y < kBlocks; ++y) {
-          uint32_t mx[4] = {0, 0, 0, 0};  // independent chains
+          uint32_t far[4] = {0, 0, 0, 0};  // independent chains
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
-            mx[0] = max_abs_bf16x2(mx[0], x[y][i].x);
-            mx[1] = max_abs_bf16x2(mx[1], x[y][i].y);
-            mx[2] = max_abs_bf16x2(mx[2], x[y][i].z);
-            mx[3] = max_abs_bf16x2(mx[3], x[y][i].w);
+            far[0] = range_max(far[0], x[y][i].x);
+            far[1] = range_max(far[1], x[y][i].y);
+            far[2] = range_max(far[2], x[y][i].z);
+            far[3] = range_max(far[3], x[y][i].w);
           }
-          mx[0] = max_abs_bf16x2(max_abs_bf16x2(mx[0], mx[1]), max_abs_bf16x2(mx[2], mx[3]));
-          mx[0] &= 0x7fff7fffu;
-          const uint32_t m = __reduce_max_sync(0xffffffffu, max(mx[0] & 0xffffu, mx[0] >> 16));
-          // bf16 bits: 2^16 is 0x4780, 2^-8 is 0x3b80; a NaN is one in fp16 too
-          f16[y] = m == 0 || (m >= 0x3b80u && m < 0x4780u);
-          if (f16[y]) {
+          const uint32_t f = __vmaxu2(__vmaxu2(far[0], far[1]), __vmaxu2(far[2], far[3]));
+          constexpr uint32_t kMost = kPair * (2 * (kBelow - kNormal) - 1);
+          direct[y] = __all_sync(0xffffffffu, __vmaxu2(f, kMost) == kMost);
+        }
+#pragma unroll
+        for (int y = 0; y < kBlocks; ++y) {
+          if (direct[y]) {  // all normal numbers of fp16: the exponent's low bits, moved
+            f16[y] = true;
+            const auto turn = [&](uint32_t v) {
+              return (((v & 0x0fff0fffu) * 8 + kMove) & 0x7fff7fffu) | (v & 0x80008000u);
+            };
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
               uint4& v = x[y][i];
-              v.x = pack_f16x2(bf16_lo_to_float(v.x), bf16_hi_to_float(v.x));
-              v.y = pack_f16x2(bf16_lo_to_float(v.y), bf16_hi_to_float(v.y));
-              v.z = pack_f16x2(bf16_lo_to_float(v.z), bf16_hi_to_float(v.z));
-              v.w = pack_f16x2(bf16_lo_to_float(v.w), bf16_hi_to_float(v.w));
+              v = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
+            }
+          } else {  // some are zeros or fp16's subnormal numbers, or out of its range
+            uint32_t far = 0;
+            const auto take = [&](uint32_t w) {  // (a 0 counts as the smallest in range)
+              const uint32_t m = w & 0x7fff7fffu;
+              far = __vmaxu2(far, __vsub2(m, kPair * kFrom) & ~__vcmpeq2(m, 0));
+            };
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+              take(x[y][i].x);
+              take(x[y][i].y);
+              take(x[y][i].z);
+              take(x[y][i].w);
+            }
+            f16[y] = __all_sync(0xffffffffu, max(far & 0xffffu, far >> 16) < kBelow - kFrom);
+            if (f16[y]) {
+              const auto turn = [&](uint32_t v) {
+                v += kTimes;
+                return pack_f16x2(bf16_lo_to_float(v), bf16_hi_to_float(v));
+              };
+#pragma unroll
+              for (int i = 0; i < kWords; ++i) {
+                uint4& v = x[y][i];
+                v = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
+              }
             }
           }
 #pragma unroll
@@ -696,10 +742,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 } else {
                   e0 = round17(e0);
                   e1 = round17(e1);
-                  split_hi_lo(e0, e1, hi[u], lo[u]);
+                  split_hi_lo(e0 * kChValueScale, e1 * kChValueScale, hi[u], lo[u]);
                   t0 = round17(e0 * t0);
                   t1 = round17(e1 * t1);
-                  split_hi_lo(t0, t1, thi[u], tlo[u]);
+                  split_hi_lo(t0 * kChValueScale, t1 * kChValueScale, thi[u], tlo[u]);
                 }
                 lt[y] = f2_add(lt[y], f2_pack(e0, e1));
                 bt[y] = f2_add(bt[y], f2_pack(t0, t1));
@@ -761,8 +807,11 @@ __global__ void __launch_bounds__(kChThreads, 1)
       tc_fence_after_sync();
       const bool live = r_tok < ntok;
       const float lsum = rd[r], cs = rd[2 * kChunkRows + r] * 2048.f;
-      // l and A carry 2^11; C and b, which carry 2^sigma, are brought to it
+      // l and A carry 2^11; C and b, which carry 2^sigma, are brought to it. The
+      // values' 2^8 leaves A and C here.
       const float bfull = PROBE ? rd[kChunkRows + r] * cs : 0.f;
+      constexpr float kUnscale = 1.f / kChValueScale;
+      const float c_unscale = cs * kUnscale;
       const float inv = lsum > 0.f ? 1.f / lsum : 0.f, bl = bfull * inv;
       const size_t orow =
           ((size_t)(pc.s.s0 + j0 + r_tok) * p.Hq + (size_t)pc.g * p.G + r_head) * D;
@@ -788,8 +837,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
               float o2[2];
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
-                const float vbar = a[x + y + z] * inv;
-                o2[z] = PROBE ? vbar + (cc[x + y + z] * cs * inv - bl * vbar) : vbar;
+                const float vbar = a[x + y + z] * kUnscale * inv;
+                o2[z] = PROBE ? vbar + (cc[x + y + z] * c_unscale * inv - bl * vbar) : vbar;
               }
               w[y / 2] = pack_bf16x2(o2[0], o2[1]);
             }
@@ -800,10 +849,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             const int col = (c0 + x) / 4;
-            ra[col * kChunkRows + r] = make_float4(a[x], a[x + 1], a[x + 2], a[x + 3]);
+            ra[col * kChunkRows + r] = make_float4(a[x] * kUnscale, a[x + 1] * kUnscale,
+                                                   a[x + 2] * kUnscale, a[x + 3] * kUnscale);
             if constexpr (PROBE)
               ra[(D / 4 + col) * kChunkRows + r] =
-                  make_float4(cc[x] * cs, cc[x + 1] * cs, cc[x + 2] * cs, cc[x + 3] * cs);
+                  make_float4(cc[x] * c_unscale, cc[x + 1] * c_unscale, cc[x + 2] * c_unscale,
+                              cc[x + 3] * c_unscale);
           }
         }
         __syncwarp();

@@ -220,14 +220,6 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   return r;
 }
 
-// Per bf16 half: the larger magnitude of a and b (its sign is theirs combined;
-// a NaN gives way to a number).
-__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // 2^x (hardware approximation; x = -inf gives +0).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;

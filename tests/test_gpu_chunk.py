@@ -431,3 +431,38 @@ def test_serving_run_together():
     o, S = reference(fq, fr, fkp, fvp, table, cu, lens, True, D ** -0.5)
     # normed, weighted probe rows: |r| about 1 per dimension and s up to 60
     check(out, o, 3 * S, max(total))
+
+
+@pytest.mark.parametrize("probe", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seqs", [[(7, 90)] * 150, [(3, 3000), (130, 200)]])
+def test_small_values_beside_ordinary_ones(seqs, D, probe):
+    """Dimensions of V that are small in every key, zero, or far, and single small
+    values in rows that a few keys dominate, in blocks whose other values are near 1:
+    S_d holds only the dimension's own values, so each has to keep its own bits.
+    Whole items (many short sequences) and cut ones."""
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, D, 117)
+    base = vp.clone()
+    f = torch.ones(D, device="cuda")
+    f[[3, 4, 5, 6, D - 1]] = torch.tensor([2.0 ** -20, 2.0 ** -30, 2.0 ** -60, 0.0, 2.0 ** 20],
+                                          device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(118)
+    few = torch.rand(vp.shape, device="cuda", generator=g) < 2e-3
+    ten = torch.rand(vp.shape, device="cuda", generator=g) < 0.1
+    for what, v, scale in (("dims", base.float() * f, D ** -0.5),
+                           ("few", torch.where(few, base.float() * 2.0 ** -28, base.float()), 1.0),
+                           ("zeros", torch.where(ten, 0.0, base.float()), D ** -0.5),
+                           ("small", base.float() * 2.0 ** -24, D ** -0.5)):
+        vp.copy_(v)
+        got = pl.parallax_prefill_paged(q, r if probe else None, kp, vp, table, lens, cu,
+                                        scale=scale, probe=probe)
+        o, S = reference(q, r if probe else None, kp, vp, table, cu, lens, True, scale)
+        check(got, o, S, 3000, what)
+
+
+def test_a_nan_among_the_values_is_not_hidden():
+    """V below the length has to be finite; a NaN there reaches the rows that see it."""
+    q, r, kp, vp, table, cu, lens = make([(2, 70)], 64, 2, 1, 64, 119, poison=False)
+    vp[table[0, 0].long(), 20, 0, 7] = float("nan")
+    out = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu)
+    assert out[:, :, 7].isnan().all() and out[:, :, :7].isfinite().all()
