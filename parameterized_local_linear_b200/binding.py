@@ -621,7 +621,8 @@ def parallax_norm_rope_append(q, r, k, v, cos_sin, k_pages, v_pages, block_table
     cache_seqlens int32 [B]: the lengths after the append. cu_seqlens_q int32
     [B + 1]: each sequence's rows, or None for one token per sequence (of length
     0: an idle row). Idle rows and rows past the last sequence have no output:
-    q_out and r_out keep what they hold there. positions int32 [tokens] or None
+    a given q_out or r_out keeps what it holds there, one that this call makes
+    holds zeros. positions int32 [tokens] or None
     (each token's key index)."""
     return _call("norm_rope_append",
                  (q, r, k, v, cos_sin, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q,

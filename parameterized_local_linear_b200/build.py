@@ -32,6 +32,7 @@ def _newer(target, files) -> bool:
 
 def up_to_date() -> bool:
     return _newer(LIB, _inputs()) and _newer(MARSHAL, [MARSHAL_SOURCE,
+                                                       os.path.join(CSRC, "internal.h"),
                                                        os.path.join(INCLUDE, "parallax.h")])
 
 
@@ -44,7 +45,7 @@ def _build_marshal() -> None:
         ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
          "-I", sysconfig.get_paths()["include"], "-I", inc,
-         "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, "-I", INCLUDE,
+         "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, "-I", INCLUDE, "-I", CSRC,
          "-o", MARSHAL + ".tmp", MARSHAL_SOURCE, "-L", lib, "-lc10", "-lc10_cuda",
          "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-L", PKG, "-l:libparallax.so", "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(MARSHAL + ".tmp", MARSHAL)

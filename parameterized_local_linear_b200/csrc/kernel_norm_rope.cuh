@@ -78,6 +78,7 @@ struct NormRopeParams {
   const int32_t *cu, *lens, *table;
   int B, page_size, num_pages, max_pages;
   NrDivisor page_div;     // by page_size
+  int clear_rest;         // zeros to the query (bit 0), probe (bit 1) rows without a token
   // backward: dy in the layout of y, dx rows dxs[i] elements apart
   const void* dy[3];
   void* dx[3];
@@ -422,7 +423,8 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   Place ahead{};  // APPEND
   if (APPEND) ahead = look_up(load_at);
   // Starts the copies of the next unit. Its note: the first row (in units of D
-  // elements) of its token's heads in the output, or -1 where it has none.
+  // elements) of its token's heads in the output, or -1 where it has none; ~row of
+  // a query or probe row without a token that is to be cleared.
   const auto load = [&](int st) {
     if (!load_at.valid()) return;
     int t, h0;
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
                 ring.bar(st));
       long long note = (long long)t * H;
       if (APPEND && f.slot < 0) {
-        note = -1;
+        note = p.clear_rest >> k & 1 ? ~note : -1;
       } else if (APPEND && k >= 2) {  // the key's place in the pools
         const bool held = f.page >= 0 && f.page < p.num_pages;
         note = held ? ((long long)f.page * p.page_size + f.slot) * H : -1;
@@ -512,6 +514,13 @@ __global__ void __launch_bounds__(kNrThreads, 2)
         }
         out += kGroups * head_step;
         row += kGroups * D;
+      }
+    } else if (APPEND && (p.clear_rest >> k & 1)) {
+      const f32x2 zero[4] = {0, 0, 0, 0};
+      for (int h = grp; h < n; h += kGroups) {
+        T* const out = y + ((size_t)~out_row + h0 + h) * D;
+        nr_put(out + 8 * ln.a, zero);
+        nr_put(out + 8 * ln.b, zero);
       }
     }
     __syncwarp();  // the warp is done with this stage

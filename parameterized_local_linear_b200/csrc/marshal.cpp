@@ -16,6 +16,7 @@
 #include <stdexcept>
 #include <string>
 
+#include "internal.h"
 #include "parallax.h"
 
 namespace {
@@ -299,14 +300,16 @@ PyObject* norm_rope_append(PyObject* const* a) {
   const Pool pool(x.c, a[5], a[6], a[7], len.B, x.Hkv);
   const Tensor qo = x.c.output(a[16], "q_out", {x.n, x.Hq, x.D});
   const Tensor ro = x.r ? x.c.output(a[17], "r_out", {x.n, x.Hq, x.D}) : Tensor();
+  // rows without a token: zeros in an output made here, untouched in a given one
+  const int clear = (a[16] == Py_None ? 1 : 0) | (x.r && a[17] == Py_None ? 2 : 0);
   const Tensor ws = x.c.workspace(a[18], 256);
-  check(parallax_norm_rope_append(
+  check(parallax_internal_norm_rope_append(
             x.c.q.data_ptr(), ptr(x.r), x.k.data_ptr(), v.data_ptr(), x.qw, x.rw, x.kw,
             static_cast<const float*>(x.cs.data_ptr()), x.pos, len.cu, len.lens, pool.ids(),
             qo.data_ptr(), x.r ? ro.data_ptr() : nullptr, pool.k.data_ptr(), pool.v.data_ptr(),
             len.B, x.n, x.Hq, x.Hkv, x.D, x.rot, integer(a[15]) != 0, x.max_pos,
             (float)number(a[14]), x.sq, x.sr, x.sk, sv, pool.pages(), pool.page_size(),
-            pool.max_pages(), x.dtype, x.c.stream(), ws.data_ptr(), (size_t)ws.numel()),
+            pool.max_pages(), x.dtype, x.c.stream(), ws.data_ptr(), (size_t)ws.numel(), clear),
         "parallax_norm_rope_append");
   return tuple({wrap(qo), x.r ? wrap(ro) : none()});
 }

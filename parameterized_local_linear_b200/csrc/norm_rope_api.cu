@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "host.cuh"
+#include "internal.h"
 #include "kernel_norm_rope.cuh"
 
 using namespace plx;
@@ -256,7 +257,7 @@ extern "C" int parallax_qk_norm_rope_backward(
                                       : dispatch_backward<float>(p, D, interleaved != 0, s);
 }
 
-extern "C" int parallax_norm_rope_append(
+extern "C" int parallax_internal_norm_rope_append(
     const void* q, const void* r, const void* k, const void* v, const void* q_weight,
     const void* r_weight, const void* k_weight, const float* cos_sin, const int32_t* positions,
     const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, const int32_t* block_table,
@@ -264,7 +265,7 @@ extern "C" int parallax_norm_rope_append(
     int Hkv, int D, int rotary_dim, int interleaved, int max_positions, float eps,
     long long q_stride, long long r_stride, long long k_stride, long long v_stride, int num_pages,
     int page_size, int max_pages_per_seq, int dtype, void* stream, void* workspace,
-    size_t workspace_bytes) {
+    size_t workspace_bytes, int clear_rest) {
   int st = check_common(total_tokens, Hq, Hkv, D, rotary_dim, max_positions, eps, dtype, cos_sin,
                         positions, workspace, workspace_bytes, kWorkspaceHeaderBytes);
   if (st != PARALLAX_OK) return st;
@@ -298,5 +299,22 @@ extern "C" int parallax_norm_rope_append(
   p.page_div = NrDivisor::of(page_size);
   p.num_pages = num_pages;
   p.max_pages = max_pages_per_seq;
+  p.clear_rest = clear_rest & 3;
   return dispatch_forward<true>(p, D, interleaved, dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int parallax_norm_rope_append(
+    const void* q, const void* r, const void* k, const void* v, const void* q_weight,
+    const void* r_weight, const void* k_weight, const float* cos_sin, const int32_t* positions,
+    const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, const int32_t* block_table,
+    void* q_out, void* r_out, void* k_pages, void* v_pages, int B, int total_tokens, int Hq,
+    int Hkv, int D, int rotary_dim, int interleaved, int max_positions, float eps,
+    long long q_stride, long long r_stride, long long k_stride, long long v_stride, int num_pages,
+    int page_size, int max_pages_per_seq, int dtype, void* stream, void* workspace,
+    size_t workspace_bytes) {
+  return parallax_internal_norm_rope_append(
+      q, r, k, v, q_weight, r_weight, k_weight, cos_sin, positions, cu_seqlens_q, cache_seqlens,
+      block_table, q_out, r_out, k_pages, v_pages, B, total_tokens, Hq, Hkv, D, rotary_dim,
+      interleaved, max_positions, eps, q_stride, r_stride, k_stride, v_stride, num_pages,
+      page_size, max_pages_per_seq, dtype, stream, workspace, workspace_bytes, 0);
 }

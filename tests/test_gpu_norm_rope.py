@@ -419,3 +419,36 @@ def test_streams_graphs_and_devices_context():
     for _, out, grads, _ in graphs:
         assert all(torch.equal(a, b) for a, b in zip(want, out))
         assert all(torch.equal(a, b) for a, b in zip(wantg, grads))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 16, 8), (64, 6, 2)])
+def test_append_made_outputs_hold_zeros_without_a_token(D, Hq, Hkv, dtype):
+    """Padding rows (also in front) and idle rows of outputs that the call allocates,
+    from memory that held NaN before; a given output keeps them."""
+    seqs, ps, n = [(1, 5), (0, 9), (30, 33), (1, 16)], 16, 60
+    kp, vp, table, cu, lens = make_cache(seqs, ps, Hkv, D, dtype, seed=120)
+    (q, r, k, v), w, _, cs = inputs(n, Hq, Hkv, D, D, dtype, seed=121)
+
+    def run(cu, lens, m, **out):
+        junk = [torch.full((m, Hq, D), float("nan"), device="cuda", dtype=dtype) for _ in range(8)]
+        del junk
+        return pl.parallax_norm_rope_append(q[:m], r[:m], k[:m], v[:m], cs, kp, vp, table, lens, cu,
+                                            None, *w, **out)
+
+    kept = lambda m: torch.full((m, Hq, D), 3.0, device="cuda", dtype=dtype)
+    one = torch.tensor([5, 0, 33, 0], dtype=torch.int32, device="cuda")
+    for c, nn, m, live in ((cu + 7, lens, n, range(7, 39)), (None, one, 4, (0, 2))):
+        rest = torch.ones(m, dtype=torch.bool)
+        rest[list(live)] = False
+        rest = rest.cuda()
+        a, b = run(c, nn, m)
+        given = run(c, nn, m, q_out=kept(m), r_out=kept(m))
+        half = run(c, nn, m, q_out=kept(m)), run(c, nn, m, r_out=kept(m))
+        assert not a[rest].any() and not b[rest].any()
+        assert (given[0][rest] == 3).all() and (given[1][rest] == 3).all()
+        assert (half[0][0][rest] == 3).all() and not half[0][1][rest].any()
+        assert not half[1][0][rest].any() and (half[1][1][rest] == 3).all()
+        for x in (given, *half):
+            assert torch.equal(x[0][~rest], a[~rest]) and torch.equal(x[1][~rest], b[~rest])
+        assert a[~rest].isfinite().all() and b[~rest].isfinite().all()
