@@ -591,10 +591,50 @@ def parallax_qk_norm_rope(q, r, k, cos_sin, positions=None, q_weight=None, r_wei
     cos_sin as parallax_rope_table gives it, positions int32 [tokens] or None
     (0, 1, ... in each row of seq_len tokens). Returns (q, r, k), contiguous
     [tokens, H, D], or with seq_len = L [tokens / L, H, L, D]; out: three
-    tensors to write (a q that is contiguous may be its own output)."""
-    return _call("qk_norm_rope",
-                 (q, r, k, cos_sin, positions, q_weight, r_weight, k_weight, eps, interleaved,
-                  seq_len, out, _workspace_buffer(workspace)), stream)
+    tensors to write (a q that is contiguous may be its own output).
+
+    Differentiable once in q, r, k and the weights (parallax_qk_norm_rope_backward);
+    a weight's gradient has its dtype. Without a place in autograd, and refused
+    where a gradient is wanted: out, and a cos_sin that requires one."""
+    args = (q, r, k, cos_sin, positions, q_weight, r_weight, k_weight, eps, interleaved, seq_len,
+            out, _workspace_buffer(workspace))
+    got = _call("qk_norm_rope", args, stream)
+    if got is not None:
+        return got
+    if out is not None:
+        raise ValueError("out cannot be given where autograd follows the call")
+    if cos_sin.requires_grad:
+        raise ValueError("cos_sin has no gradient")
+    if stream is None:
+        return _NormRope.apply(*args)
+    with torch.cuda.stream(_stream_on(q.device, stream)):
+        return _NormRope.apply(*args)
+
+
+class _NormRope(torch.autograd.Function):
+    """parallax_qk_norm_rope joined with its backward pass."""
+
+    @staticmethod
+    def forward(ctx, q, r, k, cos_sin, positions, q_weight, r_weight, k_weight, *rest):
+        ctx.save_for_backward(q, r, k, cos_sin, positions, q_weight, r_weight, k_weight)
+        ctx.eps, ctx.interleaved, ctx.seq_len = rest[:3]
+        return _call("qk_norm_rope",
+                     (q, r, k, cos_sin, positions, q_weight, r_weight, k_weight, *rest), None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        x = ctx.saved_tensors
+        grads = [None if x[i] is None else _dense16(g) for i, g in enumerate(grads)]
+        got = parallax_qk_norm_rope_backward(*grads, *x, ctx.eps, ctx.interleaved, ctx.seq_len)
+        dw = [None if d is None else d.to(w.dtype) for d, w in zip(got[3:], x[5:])]
+        return (*got[:3], None, None, *dw, None, None, None, None, None)
+
+
+def _dense16(t):
+    """t contiguous, at an address that the kernels take."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 def parallax_qk_norm_rope_backward(dq_out, dr_out, dk_out, q, r, k, cos_sin, positions=None,
@@ -605,7 +645,7 @@ def parallax_qk_norm_rope_backward(dq_out, dr_out, dk_out, q, r, k, cos_sin, pos
     dr_weight, dk_weight) from the gradients of its outputs (in their layout)
     and its inputs. The rows' gradients are [tokens, H, D] in q's dtype (out:
     three tensors to write, token rows as free as q's), the weights' fp32 [D],
-    None where the weight or r is None."""
+    None where the weight or r is None. Not differentiable itself."""
     return _call("qk_norm_rope_backward",
                  (dq_out, dr_out, dk_out, q, r, k, cos_sin, positions, q_weight, r_weight, k_weight,
                   eps, interleaved, seq_len, out, _workspace_buffer(workspace)), stream)
@@ -623,7 +663,7 @@ def parallax_norm_rope_append(q, r, k, v, cos_sin, k_pages, v_pages, block_table
     0: an idle row). Idle rows and rows past the last sequence have no output:
     a given q_out or r_out keeps what it holds there, one that this call makes
     holds zeros. positions int32 [tokens] or None
-    (each token's key index)."""
+    (each token's key index). Not differentiable: the outputs carry no graph."""
     return _call("norm_rope_append",
                  (q, r, k, v, cos_sin, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q,
                   positions, q_weight, r_weight, k_weight, eps, interleaved, q_out, r_out,
@@ -637,7 +677,8 @@ def parallax_prefill_paged(q, r, k_pages, v_pages, block_table, cache_seqlens, c
     q, r [tokens, Hq, D] bf16, sequence b's rows cu_seqlens_q[b]:cu_seqlens_q[b+1]
     (None: one token per sequence), the last of its cache_seqlens[b] keys.
     causal: row j of c sees keys up to its own. Rows past the last sequence are
-    left as they are (zero when this call makes the output)."""
+    left as they are (zero when this call makes the output). Not differentiable:
+    the output carries no graph."""
     return _call("prefill_paged",
                  (q, r, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q, scale, causal,
                   probe, out, _workspace_buffer(workspace)), stream)

@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -198,8 +199,18 @@ struct Out3 {
   }
 };
 
-// q, r, k, cos_sin, positions, 3 weights, eps, interleaved, seq_len, out, workspace
+// Whether autograd has to follow a call on these arguments.
+bool wants_grad(std::initializer_list<PyObject*> xs) {
+  if (!at::GradMode::is_enabled()) return false;
+  for (PyObject* o : xs)
+    if (THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad()) return true;
+  return false;
+}
+
+// q, r, k, cos_sin, positions, 3 weights, eps, interleaved, seq_len, out, workspace;
+// returns None, and does nothing, where autograd has to follow the call.
 PyObject* qk_norm_rope(PyObject* const* a) {
+  if (wants_grad({a[0], a[1], a[2], a[3], a[5], a[6], a[7]})) return none();
   Rope x(a[0], a[1], a[2], a[3], a[4], a + 5, integer(a[10]));
   const Out3 out(a[11]);
   const auto sq = x.shape(x.Hq), sk = x.shape(x.Hkv);

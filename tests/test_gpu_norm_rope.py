@@ -452,3 +452,121 @@ def test_append_made_outputs_hold_zeros_without_a_token(D, Hq, Hkv, dtype):
         for x in (given, *half):
             assert torch.equal(x[0][~rest], a[~rest]) and torch.equal(x[1][~rest], b[~rest])
         assert a[~rest].isfinite().all() and b[~rest].isfinite().all()
+
+
+# ---------------------------------------------------------------- autograd --
+def leaves(n, Hq, Hkv, D, dtype, seed):
+    """One fused projection's rows and the weights, all requiring gradients."""
+    (q, r, k, v), w, pos, cs = inputs(n, Hq, Hkv, D, D, dtype, seed)
+    x = torch.cat([q, r, k, v], 1).requires_grad_()
+    return x, [t.requires_grad_() for t in w], pos, cs, [Hq, Hq, Hkv, Hkv]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("L", [0, 10])
+def test_autograd_gives_the_backward_passes_gradients(L, dtype):
+    """Through slices of a fused projection: x.grad is the slices' gradients, each
+    weight's its own in the weight's type, and the outputs are those without autograd."""
+    n, Hq, Hkv, D = 30, 4, 2, 64
+    x, w, pos, cs, heads = leaves(n, Hq, Hkv, D, dtype, 130)
+    pos = None if L else pos
+    q, r, k, _ = x.split(heads, 1)
+    out = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, seq_len=L)
+    with torch.no_grad():
+        plain = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, seq_len=L)
+    assert all(torch.equal(a, b) and a.requires_grad and not b.requires_grad
+               for a, b in zip(out, plain))
+    g = torch.Generator(device="cuda").manual_seed(131)
+    dy = [torch.randn(o.shape, device="cuda", generator=g).to(dtype) for o in out]
+    torch.autograd.backward(out, dy)
+    with torch.no_grad():
+        want = pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w, seq_len=L)
+    for a, b in zip(x.grad.split(heads, 1), want[:3]):
+        assert torch.equal(a, b)
+    assert not x.grad[:, -Hkv:].any()
+    for t, b in zip(w, want[3:]):
+        assert t.grad.dtype == dtype and torch.equal(t.grad, b.to(dtype))
+
+
+def test_autograd_of_some_inputs_and_outputs():
+    """Without a probe, weights that want no gradient, an output that is not used,
+    and gradients that are broadcast or not aligned."""
+    n, Hq, Hkv, D = 9, 4, 2, 64
+    (q, r, k, _), w, pos, cs = inputs(n, Hq, Hkv, D, D, torch.float32, seed=132, fused=False)
+    q.requires_grad_()
+    w[2].requires_grad_()
+    ones = lambda H: torch.ones(n, H, D, device="cuda")
+    oq, o_r, ok = pl.parallax_qk_norm_rope(q, None, k, cs, pos, w[0], None, w[2])
+    assert o_r is None
+    oq.sum().backward()  # an expanded gradient; ok is not used
+    with torch.no_grad():
+        want = pl.parallax_qk_norm_rope_backward(ones(Hq), None, torch.zeros_like(k), q, None, k, cs,
+                                                 pos, w[0], None, w[2])
+    assert torch.equal(q.grad, want[0]) and not w[2].grad.any() and w[0].grad is None
+    odd = torch.zeros(n * Hkv * D + 1, device="cuda")[1:].view(n, Hkv, D).copy_(ones(Hkv))
+    assert odd.data_ptr() % 16
+    out = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w)
+    (dk,) = torch.autograd.grad(out[2], [w[2]], odd)
+    with torch.no_grad():
+        want = pl.parallax_qk_norm_rope_backward(torch.zeros_like(q), torch.zeros_like(r), ones(Hkv),
+                                                 q, r, k, cs, pos, *w)
+    assert torch.equal(dk, want[5])
+    # weights without a norm on the probe, and a stream of its own
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    r.requires_grad_()
+    out = pl.parallax_qk_norm_rope(q, r, k, cs, pos, w[0], None, w[2], stream=s)
+    s.synchronize()
+    (dr,) = torch.autograd.grad(out[1], [r], ones(Hq))
+    torch.cuda.synchronize()
+    with torch.no_grad():
+        want = pl.parallax_qk_norm_rope_backward(torch.zeros_like(q), ones(Hq), torch.zeros_like(k),
+                                                 q, r, k, cs, pos, w[0], None, w[2])
+    assert torch.equal(dr, want[1])
+
+
+def test_autograd_refusals():
+    (q, r, k, _), w, pos, cs = inputs(5, 4, 2, 64, 64, torch.float32, seed=133, fused=False)
+    w[0].requires_grad_()
+    out = tuple(torch.empty_like(x) for x in (q, r, k))
+    with pytest.raises(ValueError):
+        pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, out=out)
+    with pytest.raises(ValueError):
+        pl.parallax_qk_norm_rope(q, r, k, cs.clone().requires_grad_(), pos, *w)
+    with torch.no_grad():
+        pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, out=out)
+    # once differentiable
+    oq, _, _ = pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w)
+    (g,) = torch.autograd.grad(oq.square().sum(), [w[0]], create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
+def test_autograd_captured_in_a_graph():
+    """Forward and gradients in one graph, replayed on other inputs, while an eager
+    graph of the same leaves lives on another stream. (One on the default stream
+    breaks the capture of any operator's gradients: torch keeps a leaf's accumulation
+    on the stream where it was first used.)"""
+    n, Hq, Hkv, D = 200, 8, 4, 128
+    x, w, pos, cs, heads = leaves(n, Hq, Hkv, D, torch.bfloat16, 134)
+    dy = [torch.randn(n, H, D, device="cuda").bfloat16() for H in heads[:3]]
+
+    def step():
+        out = pl.parallax_qk_norm_rope(*x.split(heads, 1)[:3], cs, pos, *w)
+        return out, torch.autograd.grad(out, [x, *w], dy)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        alive, _ = step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, grads = step()
+    for _ in range(2):
+        with torch.no_grad():
+            x.copy_(x.roll(3, 0))
+        graph.replay()
+        want_out, want = step()
+        assert all(torch.equal(a, b) for a, b in zip((*out, *grads), (*want_out, *want)))
+    assert alive[0].requires_grad
