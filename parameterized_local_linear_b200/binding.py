@@ -163,15 +163,21 @@ class Workspace:
 
     def status(self, clear: bool = False):
         """(status code, device status bits); synchronises the device."""
-        torch.cuda.synchronize(self.buffer.device)
+        return parallax_workspace_status(self.buffer, clear)
+
+
+def parallax_workspace_status(workspace, clear: bool = False):
+    """(status code, device status bits) of a Workspace or of a workspace tensor
+    (status_workspace, prefill_workspace and the like); synchronises the device."""
+    buf = _workspace_buffer(workspace)
+    if not buf.is_cuda or buf.dtype != torch.uint8 or not buf.is_contiguous() or buf.numel() < 256:
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor of 256 bytes or more")
+    with torch.cuda.device(buf.device):
+        torch.cuda.synchronize()
         word = ctypes.c_uint32(0)
-        rc = load_library().parallax_workspace_status(ctypes.c_void_p(self.ptr()), int(clear),
+        rc = load_library().parallax_workspace_status(ctypes.c_void_p(buf.data_ptr()), int(clear),
                                                       ctypes.byref(word))
-        return rc, word.value
-
-
-def parallax_workspace_status(workspace: Workspace, clear: bool = False):
-    return workspace.status(clear)
+    return rc, word.value
 
 
 KV_LAYOUTS = {"bhsd": 0, "bshd": 1}

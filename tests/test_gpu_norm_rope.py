@@ -570,3 +570,17 @@ def test_autograd_captured_in_a_graph():
         want_out, want = step()
         assert all(torch.equal(a, b) for a, b in zip((*out, *grads), (*want_out, *want)))
     assert alive[0].requires_grad
+
+
+def test_status_of_the_workspaces_that_calls_take():
+    """parallax_workspace_status reads (and clears) the tensors that the norm, rotation
+    and chunk calls take, as it does a decode's Workspace."""
+    (q, r, k, _), w, pos, cs = inputs(6, 4, 2, 64, 64, torch.float32, seed=140, npos=100)
+    for ws in (pl.status_workspace("cuda"), pl.norm_rope_backward_workspace(6, 4, 2, 64, "cuda"),
+               pl.prefill_paged_workspace(1, 6, 4, 2, 64, "cuda"), pl.Workspace(1, 4, 2, 64, 64)):
+        assert pl.parallax_workspace_status(ws) == (0, 0)
+        pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, workspace=ws)
+        assert pl.parallax_workspace_status(ws) == (0, 0)
+        pl.parallax_qk_norm_rope(q, r, k, cs, pos + 100, *w, workspace=ws)
+        assert pl.parallax_workspace_status(ws, clear=True) == (-13, 4)
+        assert pl.parallax_workspace_status(ws) == (0, 0)

@@ -158,3 +158,9 @@ def test_stream_of_another_device_is_refused():
         pl.parallax_rope_table(16, 64, device="cuda:0", stream=Fake("cuda:1"))
     s = Fake("cuda:1")
     assert pl._stream_on(torch.device("cuda:1"), s) is s
+
+
+def test_workspace_status_refuses_what_is_no_workspace():
+    for bad in (torch.zeros(256, dtype=torch.uint8), torch.zeros(256)):
+        with pytest.raises(ValueError):
+            pl.parallax_workspace_status(bad)
