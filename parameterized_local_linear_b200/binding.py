@@ -511,6 +511,8 @@ def _marshal():
             raise RuntimeError(f"{path} is missing: build it with "
                                "`python -m parameterized_local_linear_b200.build`")
         from . import _marshal as m
+        if m.built_for != f"built for torch {torch.__version__}":
+            raise RuntimeError(f"{path} was {m.built_for}, this is {torch.__version__}: build it again")
         _marshal_module = m
     return _marshal_module
 

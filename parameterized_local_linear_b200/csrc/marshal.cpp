@@ -386,4 +386,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// build.py looks for this text in the built module, binding.py asks for the version.
+constexpr char kBuiltFor[] = "built for torch " PLX_TORCH_VERSION;
+
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", kBuiltFor) != 0) Py_CLEAR(m);
+  return m;
+}
