@@ -55,6 +55,17 @@ int parallax_testing_prefill_paged_stalled(
     void* stream, int num_pages, int page_size, int max_pages_per_seq, int probe, void* workspace,
     size_t workspace_bytes, int timeout_ms);
 
+/*
+ * Changes the next call that this host thread makes of parallax_qk_norm_rope, its
+ * backward pass or parallax_norm_rope_append (and that passes its argument checks):
+ * every wait is bounded by timeout_ms (1 .. 10000), and the first rows of each kind of
+ * head are never loaded, so that the wait of the warp that has them runs out. It records
+ * PARALLAX_DEVICE_STATUS_TIMEOUT, waits (bounded) for its own copies in flight and leaves
+ * its rows unwritten; the other warps finish theirs. Returns PARALLAX_ERR_BAD_SHAPE for a
+ * timeout outside the range.
+ */
+int parallax_testing_norm_rope_stall_next(int timeout_ms);
+
 #ifdef __cplusplus
 }
 #endif

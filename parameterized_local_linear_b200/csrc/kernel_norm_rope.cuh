@@ -38,7 +38,6 @@ namespace plx {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrWarps = kNrThreads / 32;
-constexpr unsigned long long kNrTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr unsigned int kNrStatusClamped = 2u;   // PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED
 constexpr unsigned int kNrStatusPosition = 4u;  // PARALLAX_DEVICE_STATUS_POSITION_CLAMPED
 
@@ -86,6 +85,8 @@ struct NormRopeParams {
   float* partial;         // [blocks][D] sums of dz xh
   unsigned int* done;     // [3] blocks of each kind whose partials are written
   float* dw[3];
+  unsigned long long timeout_ns;  // of each wait
+  int debug_skip_unit;            // testing hook: a unit of each kind whose rows are never loaded
 };
 
 // The two 8-value chunks a lane holds of a D-value row, and which of them the
@@ -304,6 +305,23 @@ struct NrBatch {
   }
 };
 
+// A unit of work is up to `rows` heads of one kind and token. A warp's units
+// are `stride` apart.
+struct NrUnits {
+  int unit, stride, count, rows;
+  NrDivisor per_token;
+  __device__ NrUnits(int first, int stride_, int tokens, const NrDivisor& per, int rows_)
+      : unit(first), stride(stride_), rows(rows_), per_token(per) {
+    count = tokens * (int)per.d;  // below 2^31: the entry points check tokens x heads
+  }
+  __device__ bool valid() const { return unit < count; }
+  __device__ void place(int& t, int& h0) const {
+    t = per_token.quotient(unit);
+    h0 = (unit - t * (int)per_token.d) * rows;
+  }
+  __device__ void next() { unit = count - unit > stride ? unit + stride : count; }
+};
+
 // The ring of one warp: kStages stages of PARTS x BYTES of head rows, a table
 // row (up to 512 bytes) and a note, filled by bulk copies that an mbarrier per
 // stage counts.
@@ -328,33 +346,23 @@ struct NrRing {
     for (int st = 0; st < STAGES; ++st) mbar_init(bar(st), 1);
     mbar_fence_init();
   }
-  // Waits for a stage's copies. Where they do not land, reports it, gives the
-  // other stages' (parities as the ring's walk left them) as long and fails.
-  __device__ bool wait(int st, uint32_t parity, unsigned int* status) const {
-    const bool got = mbar_wait_bounded(bar(st), parity, kNrTimeoutNs, nullptr);
+  // Waits for the copies of a unit. Where they do not land, reports it, gives those
+  // of the units after it as long (the ones started: up to STAGES - 1) and fails.
+  __device__ bool wait(int st, uint32_t parity, NrUnits at, const NormRopeParams& p) const {
+    const bool got = mbar_wait_bounded(bar(st), parity, p.timeout_ns, nullptr);
     if (__all_sync(0xffffffffu, got)) return true;  // (the warp goes on or gives up as one)
-    atomicOr(status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
-    for (int s = 0; s < STAGES; ++s)
-      if (s != st) mbar_wait_bounded(bar(s), s > st ? parity : parity ^ 1, kNrTimeoutNs, nullptr);
+    atomicOr(p.status, 1u /* PARALLAX_DEVICE_STATUS_TIMEOUT */);
+    for (int i = 1; i < STAGES; ++i) {
+      at.next();
+      if (!at.valid()) break;
+      if (++st == STAGES) {
+        st = 0;
+        parity ^= 1;
+      }
+      mbar_wait_bounded(bar(st), parity, p.timeout_ns, nullptr);
+    }
     return false;
   }
-};
-
-// A unit of work is up to `rows` heads of one kind and token. A warp's units
-// are `stride` apart.
-struct NrUnits {
-  int unit, stride, count, rows;
-  NrDivisor per_token;
-  __device__ NrUnits(int first, int stride_, int tokens, const NrDivisor& per, int rows_)
-      : unit(first), stride(stride_), rows(rows_), per_token(per) {
-    count = tokens * (int)per.d;  // below 2^31: the entry points check tokens x heads
-  }
-  __device__ bool valid() const { return unit < count; }
-  __device__ void place(int& t, int& h0) const {
-    t = per_token.quotient(unit);
-    h0 = (unit - t * (int)per_token.d) * rows;
-  }
-  __device__ void next() { unit = count - unit > stride ? unit + stride : count; }
 };
 
 // 4 KB of rows per stage: 16 heads of 128 bf16 dimensions. Two blocks per SM
@@ -455,7 +463,14 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     if (APPEND) ahead = look_up(load_at);
   };
 #pragma unroll 1
-  for (int st = 0; st < kSt; ++st) load(st);
+  for (int st = 0; st < kSt; ++st) {
+    if (load_at.unit != p.debug_skip_unit) {
+      load(st);
+    } else {
+      load_at.next();
+      if (APPEND) ahead = look_up(load_at);
+    }
+  }
   __syncwarp();  // the notes (later ones: the barrier that frees each stage)
 
   f32x2 wa[4], wb[4];
@@ -471,7 +486,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   for (; at.valid(); at.next()) {
     int t, h0;
     at.place(t, h0);
-    if (!ring.wait(st, parity, p.status)) break;
+    if (!ring.wait(st, parity, at, p)) break;
     const long long out_row = *ring.note(st);
     const int n = min(at.rows, H - h0);
     if (out_row >= 0) {
@@ -602,7 +617,14 @@ __global__ void __launch_bounds__(kNrThreads, 2)
     ahead = position(load_at);
   };
 #pragma unroll 1
-  for (int st = 0; st < kSt; ++st) load(st);
+  for (int st = 0; st < kSt; ++st) {
+    if (load_at.unit != p.debug_skip_unit) {
+      load(st);
+    } else {
+      load_at.next();
+      ahead = position(load_at);
+    }
+  }
 
   f32x2 wa[4], wb[4], da[4] = {0, 0, 0, 0}, db[4] = {0, 0, 0, 0};
   if (norm) {
@@ -614,7 +636,7 @@ __global__ void __launch_bounds__(kNrThreads, 2)
   for (; at.valid(); at.next()) {
     int t, h0;
     at.place(t, h0);
-    if (!ring.wait(st, parity, p.status)) break;
+    if (!ring.wait(st, parity, at, p)) break;
     const int n = min(at.rows, H - h0);
     const NrAngles ang = nr_angles<D, INTER, true>(ring.table(st), ln, p.rot);
     T* out = dx + (size_t)t * dxs + (size_t)(h0 + grp) * D;

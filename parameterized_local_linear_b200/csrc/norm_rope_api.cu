@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "parallax.h"
+#include "parallax_testing.h"
 
 #include "common.cuh"
 #include "host.cuh"
@@ -137,6 +138,9 @@ int dispatch_backward(const NormRopeParams& p, int D, bool inter, cudaStream_t s
   return inter ? launch_backward<T, 64, true>(p, s) : launch_backward<T, 64, false>(p, s);
 }
 
+constexpr unsigned long long kNrTimeoutNs = 2000000000ull;  // 2 s per wait
+thread_local unsigned long long stalled_timeout_ns = 0;  // of the next call, if not 0
+
 NormRopeParams base_params(int tokens, int Hq, int Hkv, int rot, int max_pos, float eps,
                            const float* cs, const int32_t* pos, bool probe, void* ws) {
   NormRopeParams p{};
@@ -150,6 +154,9 @@ NormRopeParams base_params(int tokens, int Hq, int Hkv, int rot, int max_pos, fl
   p.max_pos = max_pos;
   p.eps = eps;
   p.status = static_cast<unsigned int*>(ws);
+  p.timeout_ns = stalled_timeout_ns ? stalled_timeout_ns : kNrTimeoutNs;
+  p.debug_skip_unit = stalled_timeout_ns ? 0 : -1;
+  stalled_timeout_ns = 0;
   return p;
 }
 
@@ -317,4 +324,10 @@ extern "C" int parallax_norm_rope_append(
       block_table, q_out, r_out, k_pages, v_pages, B, total_tokens, Hq, Hkv, D, rotary_dim,
       interleaved, max_positions, eps, q_stride, r_stride, k_stride, v_stride, num_pages,
       page_size, max_pages_per_seq, dtype, stream, workspace, workspace_bytes, 0);
+}
+
+extern "C" int parallax_testing_norm_rope_stall_next(int timeout_ms) {
+  if (timeout_ms < 1 || timeout_ms > 10000) return PARALLAX_ERR_BAD_SHAPE;
+  stalled_timeout_ns = (unsigned long long)timeout_ms * 1000000ull;
+  return PARALLAX_OK;
 }

@@ -584,3 +584,40 @@ def test_status_of_the_workspaces_that_calls_take():
         pl.parallax_qk_norm_rope(q, r, k, cs, pos + 100, *w, workspace=ws)
         assert pl.parallax_workspace_status(ws, clear=True) == (-13, 4)
         assert pl.parallax_workspace_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_bounded_wait_reports_and_context_survives(n):
+    """The first rows of each kind are never loaded: within the short limit the status
+    word says so (no matter how few of the ring's stages hold copies), the rows of other
+    warps are right, the backward's counters are 0 again and the next calls are right."""
+    import time
+    Hq, Hkv, D, ps = 16, 8, 128, 64
+    (q, r, k, v), w, pos, cs = inputs(n, Hq, Hkv, D, D, torch.bfloat16, seed=141)
+    dy = [torch.randn(n, H, D, device="cuda").bfloat16() for H in (Hq, Hq, Hkv)]
+    kp, vp, table, cu, lens = make_cache([(n, n)], ps, Hkv, D, torch.bfloat16, seed=142)
+    ws = pl.norm_rope_backward_workspace(n, Hq, Hkv, D, "cuda")
+    q_out = torch.empty(n, Hq, D, device="cuda", dtype=torch.bfloat16)
+    calls = (
+        lambda: pl.parallax_qk_norm_rope(q, r, k, cs, pos, *w, workspace=ws),
+        lambda: pl.parallax_qk_norm_rope_backward(*dy, q, r, k, cs, pos, *w, workspace=ws),
+        lambda: pl.parallax_norm_rope_append(q, r, k, v, cs, kp, vp, table, lens, cu, pos, *w,
+                                             q_out=q_out, r_out=torch.empty_like(q_out), workspace=ws),
+    )
+    stall = pl.load_library().parallax_testing_norm_rope_stall_next
+    for call in calls:
+        want = [x.clone() for x in call()]
+        torch.cuda.synchronize()
+        start = time.perf_counter()
+        assert stall(50) == 0
+        got = call()
+        assert pl.parallax_workspace_status(ws) == (-9, 1)
+        assert 0.04 < time.perf_counter() - start < 1.5  # 50 ms for each of at most 3 stages
+        ws[:4].zero_()
+        assert not ws[:256].any()
+        if n == 3000:  # a warp of each kind gave up, at its first unit
+            same = (got[0] == want[0]).flatten(1).all(1)
+            assert same.sum() > n * 0.9
+        again = call()
+        assert all(torch.equal(a, b) for a, b in zip(want, again))
+        assert pl.parallax_workspace_status(ws) == (0, 0)

@@ -164,3 +164,8 @@ def test_workspace_status_refuses_what_is_no_workspace():
     for bad in (torch.zeros(256, dtype=torch.uint8), torch.zeros(256)):
         with pytest.raises(ValueError):
             pl.parallax_workspace_status(bad)
+
+
+def test_stall_hook_bounds_its_timeout(lib):
+    fn = lib.parallax_testing_norm_rope_stall_next
+    assert [fn(t) for t in (0, -1, 10001)] == [ESHAPE] * 3
