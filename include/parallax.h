@@ -376,7 +376,9 @@ int parallax_varlen_prefill(const void* q, const void* r, const void* k, const v
  *  - positions [tokens] int32. A position outside [0, max_positions) is
  *    clamped into it and sets PARALLAX_DEVICE_STATUS_POSITION_CLAMPED.
  *  - eps > 0, finite. Row, weight and table pointers 16-byte aligned.
- *  - workspace: its first 256 bytes (zeroed once) hold the device status word.
+ *  - workspace: its first 256 bytes (zeroed once) hold the device status word and
+ *    the backward pass's counters (bytes 32 .. 43, 0 between calls): nothing else
+ *    is to be kept there.
  * Errors as parallax_decode (PARALLAX_ERR_BAD_SHAPE for strides, eps,
  * rotary_dim and the like).
  */
@@ -417,9 +419,12 @@ int parallax_qk_norm_rope(const void* q, const void* r, const void* k, const voi
  *   dx = (dn - xh mean(dn xh)) / sqrt(mean(x^2) + eps),  dweight = sum dz xh.
  *  - dq may be dq_out (and so on) when seq_len = 0 and dq_stride = Hq * D; no
  *    other overlap. q (r, k) is not read where its weight is NULL.
- *  - Results are bitwise reproducible (no atomics).
- *  - workspace: parallax_qk_norm_rope_backward_workspace_bytes; concurrent
- *    calls need separate workspaces.
+ *  - Results are bitwise reproducible: the weights' partial sums are added in a
+ *    fixed order by each kind's last block, which an atomic counter in the
+ *    workspace header finds. The counters must be 0 on entry and are 0 again
+ *    after the call; otherwise a weight gradient is wrong or not written.
+ *  - workspace: parallax_qk_norm_rope_backward_workspace_bytes, the first 256
+ *    bytes zeroed once; concurrent calls need separate workspaces.
  */
 int parallax_qk_norm_rope_backward(
     const void* dq_out, const void* dr_out, const void* dk_out, const void* q, const void* r,
