@@ -458,7 +458,8 @@ size_t parallax_qk_norm_rope_backward_workspace_bytes(int tokens, int Hq, int Hk
  *    sequence becomes key cache_seqlens[b] - c + j. A key outside the block
  *    table or in a page outside the pool is not written and sets
  *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED. Two tokens with one slot (a page
- *    listed for two sequences): one of them is kept.
+ *    that two sequences append to): the slot's rows then hold parts of either,
+ *    16 bytes from one of them; nothing else is affected.
  *  - positions NULL: a token's position is its key index (so that a key below 0,
  *    of a sequence shorter than its new tokens, sets
  *    PARALLAX_DEVICE_STATUS_POSITION_CLAMPED too).

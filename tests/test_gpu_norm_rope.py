@@ -621,3 +621,31 @@ def test_bounded_wait_reports_and_context_survives(n):
         again = call()
         assert all(torch.equal(a, b) for a, b in zip(want, again))
         assert pl.parallax_workspace_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_of_two_tokens_to_one_slot(dtype):
+    """Two sequences append to the same slots: each 16 bytes there are one token's or
+    the other's, every other slot and all of q and r are right."""
+    Hq, Hkv, D, ps = 16, 8, 128, 64
+    seqs = [(40, 50), (40, 50), (3, 9)]
+    kp, vp, table, cu, lens = make_cache(seqs, ps, Hkv, D, dtype, seed=150)
+    table[1] = table[0]
+    (q, r, k, v), w, _, cs = inputs(83, Hq, Hkv, D, D, dtype, seed=151)
+    idx = torch.cat([torch.arange(10, 50), torch.arange(10, 50), torch.arange(6, 9)]).int().cuda()
+    fq, fr, fk = pl.parallax_qk_norm_rope(q, r, k, cs, idx, *w)
+    before_k, before_v = kp.clone(), vp.clone()
+    ws = pl.status_workspace("cuda")
+    for _ in range(5):
+        qo, ro = pl.parallax_norm_rope_append(q, r, k, v, cs, kp, vp, table, lens, cu, None, *w,
+                                              workspace=ws)
+        assert torch.equal(qo, fq) and torch.equal(ro, fr)
+        for pool, before, x in ((kp, before_k, fk), (vp, before_v, v)):
+            part = lambda t: t.contiguous().view(torch.int32).unflatten(-1, (-1, 4))
+            got, a, b = part(pool[table[0, 0], 10:50]), part(x[:40]), part(x[40:80])
+            assert ((got == a).all(-1) | (got == b).all(-1)).all()
+            want = before.clone()
+            want[table[0, 0], 10:50] = pool[table[0, 0], 10:50]
+            want[table[2, 0], 6:9] = x[80:]
+            assert torch.equal(pool, want)
+    assert int(ws[:4].view(torch.int32)) == 0
