@@ -498,7 +498,12 @@ int parallax_norm_rope_append(
  *    keys behind the row's position. Values enter the products with all their
  *    bits; the weights e and e*s as one fp16 term each (11 bits), or as bf16
  *    hi + lo pairs (17 bits) for 16 keys one of whose values is not 0 and not
- *    in [2^-25, 2^8) in magnitude.
+ *    in [2^-25, 2^8) in magnitude. fp16 holds the 11 bits of an e down to 2^-25
+ *    of the row's largest, of an e*s down to 2^-22 of the row's largest |s|
+ *    times its largest e; smaller ones are off by at most 2^-36 and 2^-33 of
+ *    these. (So a key of weight 0 whose |s| is far above 2^22 times the others'
+ *    takes the others' bits.)
+ *  - out must not overlap any input.
  *  - A page id outside [0, num_pages) is not read: its keys are left out and
  *    PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED is set.
  *  - probe != 0: the Parallax output (r required); probe == 0: softmax.

@@ -685,7 +685,8 @@ def parallax_prefill_paged(q, r, k_pages, v_pages, block_table, cache_seqlens, c
     q, r [tokens, Hq, D] bf16, sequence b's rows cu_seqlens_q[b]:cu_seqlens_q[b+1]
     (None: one token per sequence), the last of its cache_seqlens[b] keys.
     causal: row j of c sees keys up to its own. Rows past the last sequence are
-    left as they are (zero when this call makes the output). Not differentiable:
+    left as they are (zero when this call makes the output). out must not overlap
+    an input. Not differentiable:
     the output carries no graph."""
     return _call("prefill_paged",
                  (q, r, k_pages, v_pages, block_table, cache_seqlens, cu_seqlens_q, scale, causal,

@@ -27,9 +27,11 @@
 // summed from exactly the rounded values, so the weights stay consistent.
 //  - e 2^11: the stale row maximum is kept until it is exceeded by 2^4, so the
 //    values reach 2^15 and stay normal fp16 numbers down to e = 2^-25.
-//  - e s 2^sigma: sigma is a power of two per row, set by the row's largest |s|
-//    so far (|s| 2^sigma below 2^11) and lowered with O_C and b when it grows,
-//    as O_A and l are when the maximum does.
+//  - e s 2^sigma: 2^sigma is a power of two per row, set by the row's largest |s|
+//    so far (to |s| 2^sigma in [2^8, 2^9), growing to below 2^11) and lowered with
+//    O_C and b when that grows further, as O_A and l are when the maximum does. It
+//    is never raised within a piece: e s is normal in fp16 down to 2^-22 of the
+//    largest |s|, and within 2^-33 of it below.
 //  - V: a block of 16 keys whose values are all 0 or of magnitude [2^-25, 2^8)
 //    becomes fp16, times 2^8, which is exact for every one of them (8 significant
 //    bits; fp16's last step is 2^-24). Any other block (far values, tiny ones,

@@ -466,3 +466,39 @@ def test_a_nan_among_the_values_is_not_hidden():
     vp[table[0, 0].long(), 20, 0, 7] = float("nan")
     out = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu)
     assert out[:, :, 7].isnan().all() and out[:, :, :7].isfinite().all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_far_probe_scores(D):
+    """Scores of 2^23 and 2^53 in all keys, and a key of weight 0 whose score is 2^20
+    times the others': e s of the others is then off by at most 2^-33 of the largest |s|
+    a key, so A and C by 2^-33 |s| sum |v| and their share of vbar."""
+    seqs = [(50, 230), (9, 330)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 4, 2, D, 122)
+    for e in (20, 50):
+        rr = (r.float() * 2.0 ** e).bfloat16()
+        got = pl.parallax_prefill_paged(q, rr, kp, vp, table, lens, cu)
+        o, S = reference(q, rr, kp, vp, table, cu, lens, True, D ** -0.5)
+        check(got, o, S, 330, e)
+    q[:], r[:] = 0.25 * q, 0.25 * r  # small scores, so that weights stay near each other
+    q[..., 0], r[..., 0], q[..., 1], r[..., 1] = 4.0, 0.0, 0.0, 1.0
+    kp[..., 1] = torch.where(kp[..., 1].isnan(), kp[..., 1], kp[..., 1] * 0)
+    for b, at in ((0, 5), (1, 100)):
+        page, slot = int(table[b, at // 64]), at % 64
+        kp[page, slot] = 0
+        kp[page, slot, :, 0], kp[page, slot, :, 1] = -2.0 ** 9, 2.0 ** 20
+    got = pl.parallax_prefill_paged(q, r, kp, vp, table, lens, cu, scale=0.5)
+    o, S = reference(q, r, kp, vp, table, cu, lens, True, 0.5)
+    for b, (c, n) in enumerate(seqs):
+        i = torch.arange(n, device="cuda")
+        page = table[b].long()[i // 64]
+        k, v = (x[page, i % 64].double().repeat_interleave(2, 1).transpose(0, 1) for x in (kp, vp))
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        t = q[rows].double().transpose(0, 1) @ k.transpose(1, 2) * 0.5
+        t = t.masked_fill(i > (torch.arange(c, device="cuda") + n - c)[:, None], float("-inf"))
+        w = torch.softmax(t, -1)
+        seen = (w > 0).double()
+        lost = 2.0 ** -33 * 2.0 ** 20 * w.amax(-1, keepdim=True)
+        S[rows] += (lost * (seen @ v.abs() + seen.sum(-1, keepdim=True) * (w @ v).abs())
+                    ).transpose(0, 1) / 7e-4
+    check(got, o, S, 330, "one")
