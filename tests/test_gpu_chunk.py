@@ -502,3 +502,30 @@ def test_far_probe_scores(D):
         S[rows] += (lost * (seen @ v.abs() + seen.sum(-1, keepdim=True) * (w @ v).abs())
                     ).transpose(0, 1) / 7e-4
     check(got, o, S, 330, "one")
+
+
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_single_tokens_beside_their_decode(G, D):
+    """One token per sequence through the tcgen05 kernel (cu_seqlens_q given) and
+    through the decode of the same rows, groups of up to 16: both against the
+    definition, and their correction c = o - vbar as a whole. bf16 rounding leaves an
+    element off by up to 2^-8 |o|, at random: the errors' share of c, <err, c> / <c, c>,
+    is then off by 2^-8 / sqrt(3) sqrt(sum o^2 c^2) / sum c^2, five times that at most,
+    where a loss of one part in 2^11 of C would show (2^-12 for the weights' roundings)."""
+    lens = [1, 2, 63, 64, 65, 129, 300, 777] * 4
+    seqs = [(1, n) for n in lens]
+    Hkv, Hq = 2, 2 * G
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, Hq, Hkv, D, 123, poison=False)
+    t = table.clamp_min(0)
+    o, S = reference(q, r, kp, vp, t, cu, lens, True, D ** -0.5)
+    vbar, _ = reference(q, None, kp, vp, t, cu, lens, True, D ** -0.5)
+    c = o - vbar
+    slack = 2.0 ** -12 + 5 * 2.0 ** -8 / 3 ** 0.5 * ((o * c).square().sum().sqrt() / c.square().sum())
+    for cu_ in (cu, None):
+        ws = pl.prefill_paged_workspace(len(seqs), q.shape[0], Hq, Hkv, D, q.device)
+        got = pl.parallax_prefill_paged(q, r, kp, vp, t, lens, cu_, workspace=ws)
+        check(got, o, S, 777, (G, D, cu_ is None))
+        share = ((got.double() - o) * c).sum() / c.square().sum()
+        assert abs(share) <= slack, (share, slack)
+        assert pl.parallax_workspace_status(ws) == (0, 0)
