@@ -486,7 +486,9 @@ int parallax_norm_rope_append(
  *  - cu_seqlens_q [B + 1] int32, non-decreasing: sequence b's rows. Any number
  *    per sequence, 0 included. Rows outside cu_seqlens_q[0] ..
  *    cu_seqlens_q[B]-1 are left as they are. NULL: one token per sequence
- *    (total_tokens = B); the call is then parallax_decode_paged.
+ *    (total_tokens = B), each with all its keys; the call is then
+ *    parallax_decode_paged for the groups of query heads that its TMA kernel
+ *    takes (larger ones: this kernel). A sequence without keys is no error then.
  *  - cache_seqlens [B] int32: keys held, the new tokens' included. With c new
  *    tokens, row j of sequence b attends keys 0 .. cache_seqlens[b] - c + j
  *    (causal != 0) or all cache_seqlens[b]; a row that sees no key is 0.

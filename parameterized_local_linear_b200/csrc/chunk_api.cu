@@ -92,8 +92,12 @@ int run_chunk(const void* q, const void* r, const void* k_pages, const void* v_p
       (reinterpret_cast<uintptr_t>(cu_seqlens_q) & 3u) ||
       (reinterpret_cast<uintptr_t>(cache_seqlens) & 3u))
     return PARALLAX_ERR_MISALIGNED;
-  // one token per sequence: the decode over the same cache
-  if (cu_seqlens_q == nullptr)
+  // One token per sequence: the decode over the same cache where its TMA kernel takes
+  // the group. Measured, 32 sequences of 4096 keys, 8 kv heads of 128, decode against
+  // chunk kernel: groups of 1 to 4 with the probe 88 to 90 us and 130 us, without it (to
+  // 8) 87 to 92 and 104; one sequence 7 to 9 us and 21 to 26. Larger groups, which the
+  // decode has only its generic kernel for: 4700 us against 134 (1 sequence: 105, 26).
+  if (cu_seqlens_q == nullptr && decode_on_tma(PARALLAX_DTYPE_BF16, probe, Hq / Hkv))
     return parallax_decode_paged(q, r, k_pages, v_pages, block_table, cache_seqlens, out, B, Hq,
                                  Hkv, D, scale, stream, num_pages, page_size, max_pages_per_seq,
                                  probe, PARALLAX_DTYPE_BF16, PARALLAX_DTYPE_BF16, 0, workspace,
@@ -105,7 +109,7 @@ int run_chunk(const void* q, const void* r, const void* k_pages, const void* v_p
   ChunkParams p{};
   p.G = Hq / Hkv;
   p.sp = ChunkSpace{cu_seqlens_q, cache_seqlens,       B, total_tokens, page_size * max_pages_per_seq,
-                    Hkv,          kChunkRows / p.G, causal != 0};
+                    Hkv,          kChunkRows / p.G, causal != 0 && cu_seqlens_q != nullptr};
   p.out = static_cast<__nv_bfloat16*>(out);
   p.status = static_cast<unsigned int*>(workspace);
   p.merges = reinterpret_cast<ChunkMerge*>(static_cast<char*>(workspace) + kWorkspaceHeaderBytes);

@@ -28,7 +28,7 @@ constexpr int kChunkKeys = 64;
 constexpr int kChunkItemCost = 3;
 
 struct ChunkSpace {
-  const int32_t* cu;    // [B + 1] first new token of each sequence
+  const int32_t* cu;    // [B + 1] first new token of each sequence, or NULL: one each
   const int32_t* lens;  // [B] cached keys, the new tokens' included
   int B, total, Lmax, Hkv, tpt, causal;
 };
@@ -39,8 +39,8 @@ struct ChunkSeq {
 
 __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
   ChunkSeq s;
-  s.s0 = min(max(__ldg(sp.cu + b), 0), sp.total);
-  s.q = min(max(__ldg(sp.cu + b + 1), s.s0), sp.total) - s.s0;
+  s.s0 = sp.cu ? min(max(__ldg(sp.cu + b), 0), sp.total) : b;
+  s.q = sp.cu ? min(max(__ldg(sp.cu + b + 1), s.s0), sp.total) - s.s0 : 1;
   s.n = clamp_len(__ldg(sp.lens + b), sp.Lmax);
   return s;
 }
@@ -52,7 +52,8 @@ __device__ __forceinline__ int chunk_row_tiles(const ChunkSpace& sp, const Chunk
 // A sequence whose bounds or length chunk_seq clamped, or with more new tokens
 // than keys.
 __device__ __forceinline__ bool chunk_seq_clamped(const ChunkSpace& sp, int b) {
-  const int a = __ldg(sp.cu + b), e = __ldg(sp.cu + b + 1), n = __ldg(sp.lens + b);
+  const int a = sp.cu ? __ldg(sp.cu + b) : b, e = sp.cu ? __ldg(sp.cu + b + 1) : b + 1;
+  const int n = __ldg(sp.lens + b);
   return a < 0 || e < a || e > sp.total || n < 0 || n > sp.Lmax || (sp.causal && n < e - a);
 }
 

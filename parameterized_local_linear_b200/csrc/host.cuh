@@ -38,6 +38,12 @@ inline int current_sm_count(int* out) {
   return PARALLAX_OK;
 }
 
+// Whether the TMA decode kernel has room for a group of G query heads per kv head
+// (8 columns for their queries and probes); else the generic kernel runs.
+inline bool decode_on_tma(int in_dtype, int probe, int G) {
+  return in_dtype == PARALLAX_DTYPE_BF16 && (probe ? 2 * G <= 8 : G <= 8);
+}
+
 // --------------------------------------------------------- TMA descriptors --
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {

@@ -399,7 +399,7 @@ int run_cluster(const Call& c, const DecodeParams& prm, int S) {
 // probe) fits its 8 mma columns; everything else runs on the generic kernel.
 bool tma_path(const Call& c) {
   const int G = c.Hkv > 0 ? c.Hq / c.Hkv : 0;
-  return c.in_dtype == PARALLAX_DTYPE_BF16 && (c.probe ? 2 * G <= 8 : G <= 8);
+  return decode_on_tma(c.in_dtype, c.probe, G);
 }
 
 template <bool PROBE, bool OUT_F32>

@@ -529,3 +529,28 @@ def test_single_tokens_beside_their_decode(G, D):
         share = ((got.double() - o) * c).sum() / c.square().sum()
         assert abs(share) <= slack, (share, slack)
         assert pl.parallax_workspace_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("probe", [True, False])
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 16), (64, 5), (128, 128)])
+def test_one_token_form_of_large_groups(D, G, probe):
+    """Groups that the decode's TMA kernel has no room for run on the chunk kernel, with
+    the results (bit for bit) of the same call with cu_seqlens_q; sequences without
+    keys are zeros and no error."""
+    seqs = [(1, n) for n in (300, 1, 0, 64, 129, 0, 2000)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 2 * G, 2, D, 124)
+    ws = pl.prefill_paged_workspace(len(seqs), len(seqs), 2 * G, 2, D, q.device)
+    call = lambda c, causal=True: pl.parallax_prefill_paged(
+        q, r if probe else None, kp, vp, table, lens, c, causal=causal, probe=probe, workspace=ws)
+    if not probe and G <= 8:  # the decode takes these: values past the lengths are not read
+        kp.nan_to_num_(0.5), vp.nan_to_num_(0.5)
+        table.clamp_min_(0)
+    a = call(None)
+    assert pl.parallax_workspace_status(ws) == (0, 0)
+    o, S = reference(q, r if probe else None, kp, vp, table, cu, lens, True, D ** -0.5)
+    check(a, o, S, 2000, (D, G, probe))
+    assert not a[2].any() and not a[5].any()
+    if probe or G > 8:
+        b = call(cu, causal=False)
+        assert pl.parallax_workspace_status(ws) == (0, 0)
+        assert torch.equal(a, b) and torch.equal(a, call(None, causal=False))
