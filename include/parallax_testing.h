@@ -66,6 +66,22 @@ int parallax_testing_prefill_paged_stalled(
  */
 int parallax_testing_norm_rope_stall_next(int timeout_ms);
 
+/*
+ * The work partition of parallax_prefill_paged, walked on the host by the kernel's own
+ * arithmetic (csrc/chunk_partition.cuh). Host pointers: cu_seqlens_q [B + 1] or NULL,
+ * cache_seqlens [B]. For each of `ctas` CTAs, merges gets 5 ints (token, ntok, kv head,
+ * first range, whether that is a first piece) and pieces 8 per piece (CTA, sequence, kv
+ * head, row tile, first tile, last tile + 1, complete, first). Returns the number of
+ * pieces, or PARALLAX_ERR_BAD_SHAPE for more than max_pieces.
+ */
+int parallax_testing_chunk_walk(const int32_t* cu_seqlens_q, const int32_t* cache_seqlens, int B,
+                                int total_tokens, int Lmax, int Hkv, int tokens_per_tile,
+                                int causal, int ctas, int32_t* pieces, int max_pieces,
+                                int32_t* merges);
+
+/* n / d (0 <= n, 1 <= d) as the norm and rotation kernels compute it. */
+int parallax_testing_divide(int n, int d);
+
 #ifdef __cplusplus
 }
 #endif

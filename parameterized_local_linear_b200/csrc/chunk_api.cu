@@ -170,3 +170,43 @@ extern "C" int parallax_testing_prefill_paged_stalled(
                    max_pages_per_seq, probe, workspace, workspace_bytes,
                    (unsigned long long)timeout_ms * 1000000ull, 1);
 }
+
+extern "C" int parallax_testing_chunk_walk(const int32_t* cu_seqlens_q,
+                                           const int32_t* cache_seqlens, int B, int total_tokens,
+                                           int Lmax, int Hkv, int tokens_per_tile, int causal,
+                                           int ctas, int32_t* pieces, int max_pieces,
+                                           int32_t* merges) {
+  const ChunkSpace sp{cu_seqlens_q, cache_seqlens,   B,          total_tokens, Lmax,
+                      Hkv,          tokens_per_tile, causal != 0};
+  const auto cost = [&](const ChunkSeq& s) { return chunk_cost(sp, s, chunk_row_tiles(sp, s)); };
+  long long total = 0;
+  for (int b = 0; b < B; ++b) total += cost(chunk_seq(sp, b)) * Hkv;
+  int count = 0;
+  for (int c = 0; c < ctas; ++c) {
+    ChunkRange r{};
+    chunk_bounds(r, total, c, ctas);
+    if (r.lo < r.hi) {  // the item at r.lo, in chunk_locate's steps without its searches
+      long long rem = r.lo;
+      r.s = chunk_seq(sp, 0);
+      while (rem >= cost(r.s) * Hkv) {
+        rem -= cost(r.s) * Hkv;
+        r.s = chunk_seq(sp, ++r.b);
+      }
+      r.g = (int)div_pos(rem, cost(r.s));
+      rem -= cost(r.s) * r.g;
+      while (r.rt + 1 < chunk_row_tiles(sp, r.s) && chunk_cost(sp, r.s, r.rt + 1) <= rem) ++r.rt;
+      r.off = (int)(rem - chunk_cost(sp, r.s, r.rt));
+    }
+    const ChunkMerge mg = chunk_merge_note(sp, r);
+    const int note[5] = {mg.token, mg.ntok, mg.g, mg.c0, mg.c0_first};
+    std::copy(note, note + 5, merges + (size_t)c * 5);
+    ChunkCursor cur(r);
+    ChunkPiece pc;
+    while (cur.next(sp, pc)) {
+      if (count == max_pieces) return PARALLAX_ERR_BAD_SHAPE;
+      const int row[8] = {c, pc.b, pc.g, pc.rt, pc.t0, pc.t1, pc.complete, pc.first};
+      std::copy(row, row + 8, pieces + (size_t)count++ * 8);
+    }
+  }
+  return count;
+}

@@ -21,7 +21,18 @@
 
 #include "partition.cuh"
 
+// The arithmetic also compiles for the host, where tests walk it.
+#define PLX_HD __host__ __device__ __forceinline__
+
 namespace plx {
+
+PLX_HD int chunk_load(const int32_t* p) {
+#ifdef __CUDA_ARCH__
+  return __ldg(p);
+#else
+  return *p;
+#endif
+}
 
 constexpr int kChunkRows = 128;
 constexpr int kChunkKeys = 64;
@@ -37,15 +48,19 @@ struct ChunkSeq {
   int s0, q, n;  // first packed row, new tokens, cached keys
 };
 
-__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
+PLX_HD int chunk_clamp(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+PLX_HD int chunk_min(int a, int b) { return a < b ? a : b; }
+PLX_HD int chunk_max(int a, int b) { return a > b ? a : b; }
+
+PLX_HD ChunkSeq chunk_seq(const ChunkSpace& sp, int b) {
   ChunkSeq s;
-  s.s0 = sp.cu ? min(max(__ldg(sp.cu + b), 0), sp.total) : b;
-  s.q = sp.cu ? min(max(__ldg(sp.cu + b + 1), s.s0), sp.total) - s.s0 : 1;
-  s.n = clamp_len(__ldg(sp.lens + b), sp.Lmax);
+  s.s0 = sp.cu ? chunk_clamp(chunk_load(sp.cu + b), 0, sp.total) : b;
+  s.q = sp.cu ? chunk_clamp(chunk_load(sp.cu + b + 1), s.s0, sp.total) - s.s0 : 1;
+  s.n = clamp_len(chunk_load(sp.lens + b), sp.Lmax);
   return s;
 }
 
-__device__ __forceinline__ int chunk_row_tiles(const ChunkSpace& sp, const ChunkSeq& s) {
+PLX_HD int chunk_row_tiles(const ChunkSpace& sp, const ChunkSeq& s) {
   return (s.q + sp.tpt - 1) / sp.tpt;
 }
 
@@ -58,20 +73,20 @@ __device__ __forceinline__ bool chunk_seq_clamped(const ChunkSpace& sp, int b) {
 }
 
 // The tiles that hold the keys the last row of row tile rt sees.
-__device__ __forceinline__ int chunk_tiles(const ChunkSpace& sp, const ChunkSeq& s, int rt) {
-  const int kend = sp.causal ? s.n - s.q + min(s.q, (rt + 1) * sp.tpt) : s.n;
-  return max(1, (kend + kChunkKeys - 1) / kChunkKeys);
+PLX_HD int chunk_tiles(const ChunkSpace& sp, const ChunkSeq& s, int rt) {
+  const int kend = sp.causal ? s.n - s.q + chunk_min(s.q, (rt + 1) * sp.tpt) : s.n;
+  return chunk_max(1, (kend + kChunkKeys - 1) / kChunkKeys);
 }
 
 // sum of ceil((a + i T) / 64) over i = 1 .. m, for a >= 0: with i = 64 u + v, the
 // terms of a whole period of 64 rise by T from one period to the next. T a divisor
 // or multiple of 64 (any power of two) has a shorter one.
-__device__ __forceinline__ long long chunk_ceil_sum(int a, int T, int m) {
+PLX_HD long long chunk_ceil_sum(int a, int T, int m) {
   const int period = T >= 64 ? (T % 64 == 0 ? 1 : 64) : (64 % T == 0 ? 64 / T : 64);
   const int rise = period * T / 64;  // of a term, one period later
   const int u = m / period, v = m - u * period;
   long long sum = 0;
-  for (int i = 1; i <= min(m, period); ++i) {
+  for (int i = 1; i <= chunk_min(m, period); ++i) {
     const long long first = (a + (long long)i * T + 63) / 64;
     const long long terms = u + (i <= v ? 1 : 0);
     sum += terms * first + rise * (terms * (terms - 1) / 2);
@@ -81,7 +96,7 @@ __device__ __forceinline__ long long chunk_ceil_sum(int a, int T, int m) {
 
 // The length of the first m items of one kv head of a sequence. A loop where
 // some rows see no key (more new tokens than keys).
-__device__ __forceinline__ long long chunk_cost(const ChunkSpace& sp, const ChunkSeq& s, int m) {
+PLX_HD long long chunk_cost(const ChunkSpace& sp, const ChunkSeq& s, int m) {
   if (!sp.causal) return m * (long long)(chunk_tiles(sp, s, 0) + kChunkItemCost);
   long long c = (long long)m * kChunkItemCost;
   if (s.n < s.q) {
@@ -101,6 +116,41 @@ struct ChunkRange {
   ChunkSeq s;
   int clamped;
 };
+
+// Range c of P of a line of length total.
+PLX_HD void chunk_bounds(ChunkRange& r, long long total, int c, int P) {
+  // at least one tile past the fixed part, so that no range is all overhead (with
+  // three, fewer records but longer ranges: three short sequences 18.3 -> 19.1 us)
+  const long long per = div_pos(total + P - 1, P);
+  r.per = per > kChunkItemCost ? per : kChunkItemCost + 1;
+  r.lo = c * r.per < total ? c * r.per : total;
+  r.hi = r.lo + r.per < total ? r.lo + r.per : total;
+}
+
+// What the merge kernel does for one CTA: the item that ends in its range after
+// tiles in earlier ones. Written by the attention kernel, so that the merge
+// need not find the item again.
+struct alignas(16) ChunkMerge {
+  int token, ntok;      // first packed row and tokens of the row tile; ntok 0: nothing
+  int g;                // kv head
+  int c0, c0_first;     // the range of its first tile, and whether that is a first piece
+  int pad[3];
+};
+
+PLX_HD ChunkMerge chunk_merge_note(const ChunkSpace& sp, const ChunkRange& r) {
+  ChunkMerge mg{};
+  const int len = r.lo < r.hi ? chunk_tiles(sp, r.s, r.rt) + kChunkItemCost : 0;
+  // some of the item's tiles come before this range, and its last one in it
+  if (len > 0 && r.off > kChunkItemCost && len - r.off <= r.hi - r.lo) {
+    const long long start = r.lo - r.off;
+    mg.token = r.s.s0 + r.rt * sp.tpt;
+    mg.ntok = chunk_min(sp.tpt, r.s.q - r.rt * sp.tpt);
+    mg.g = r.g;
+    mg.c0 = (int)div_pos(start + kChunkItemCost, r.per);
+    mg.c0_first = (long long)mg.c0 * r.per >= start;
+  }
+  return mg;
+}
 
 // Warp-cooperative, no barrier: each lane sums a contiguous chunk of the
 // sequences, a scan gives the prefix, the lane whose chunk holds lo finds the
@@ -125,11 +175,7 @@ __device__ inline ChunkRange chunk_locate(const ChunkSpace& sp, int c, int P) {
   ChunkRange r{};
   r.clamped = __any_sync(0xffffffffu, clamped);
   const long long total = __shfl_sync(0xffffffffu, incl, 31);
-  // at least one tile past the fixed part, so that no range is all overhead (with
-  // three, fewer records but longer ranges: three short sequences 18.3 -> 19.1 us)
-  r.per = max((long long)kChunkItemCost + 1, div_pos(total + P - 1, P));
-  r.lo = min(total, (long long)c * r.per);
-  r.hi = min(total, r.lo + r.per);
+  chunk_bounds(r, total, c, P);
   long long pos = incl - local;
   int fb = -1;
   if (r.lo < r.hi && r.lo >= pos && r.lo < incl) {
@@ -181,19 +227,19 @@ struct ChunkCursor {
   int b, g, rt, off;
   ChunkSeq s;
 
-  __device__ explicit ChunkCursor(const ChunkRange& r)
+  __host__ __device__ explicit ChunkCursor(const ChunkRange& r)
       : pos(r.lo), lo(r.lo), hi(r.hi), b(r.b), g(r.g), rt(r.rt), off(r.off), s(r.s) {}
 
-  __device__ bool next(const ChunkSpace& sp, ChunkPiece& pc) {
+  __host__ __device__ bool next(const ChunkSpace& sp, ChunkPiece& pc) {
     while (pos < hi) {
       const int nt = chunk_tiles(sp, s, rt), len = nt + kChunkItemCost;
-      const int take = (int)min((long long)(len - off), hi - pos);
+      const int take = hi - pos < len - off ? (int)(hi - pos) : len - off;
       pc.b = b;
       pc.g = g;
       pc.rt = rt;
       pc.s = s;
-      pc.t0 = max(0, off - kChunkItemCost);
-      pc.t1 = max(0, off + take - kChunkItemCost);
+      pc.t0 = chunk_max(0, off - kChunkItemCost);
+      pc.t1 = chunk_max(0, off + take - kChunkItemCost);
       pc.complete = pc.t0 == 0 && pc.t1 == nt;
       pc.first = pos == lo;
       pos += take;

@@ -79,16 +79,6 @@ constexpr int kChConvertWarps = 2;
 constexpr int kChValueShift = 8;
 constexpr float kChValueScale = 1 << kChValueShift;
 
-// What the merge kernel does for one CTA: the item that ends in its range after
-// tiles in earlier ones. Written by the attention kernel, so that the merge
-// need not find the item again.
-struct alignas(16) ChunkMerge {
-  int token, ntok;      // first packed row and tokens of the row tile; ntok 0: nothing
-  int g;                // kv head
-  int c0, c0_first;     // the range of its first tile, and whether that is a first piece
-  int pad[3];
-};
-
 struct ChunkParams {
   ChunkSpace sp;
   __nv_bfloat16* out;      // [total][Hq][D]
@@ -204,19 +194,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       *range_slot = range;
       if (blockIdx.x == 0 && range.clamped)
         atomicOr(p.status, 2u /* PARALLAX_DEVICE_STATUS_SEQLEN_CLAMPED */);
-      ChunkMerge mg{};
-      const int len =
-          range.lo < range.hi ? chunk_tiles(p.sp, range.s, range.rt) + kChunkItemCost : 0;
-      // some of the item's tiles come before this range, and its last one in it
-      if (len > 0 && range.off > kChunkItemCost && len - range.off <= range.hi - range.lo) {
-        const long long start = range.lo - range.off;
-        mg.token = range.s.s0 + range.rt * p.sp.tpt;
-        mg.ntok = min(p.sp.tpt, range.s.q - range.rt * p.sp.tpt);
-        mg.g = range.g;
-        mg.c0 = (int)div_pos(start + kChunkItemCost, range.per);
-        mg.c0_first = (long long)mg.c0 * range.per >= start;
-      }
-      p.merges[blockIdx.x] = mg;
+      p.merges[blockIdx.x] = chunk_merge_note(p.sp, range);
     }
   }
   __syncthreads();

@@ -53,8 +53,13 @@ struct NrDivisor {
     r.m = (uint32_t)((((1ull << r.s) - d) << 32) / d + 1);
     return r;
   }
-  __device__ int quotient(int n) const {
-    return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s);
+  __host__ __device__ int quotient(int n) const {
+#ifdef __CUDA_ARCH__
+    const uint32_t hi = __umulhi(m, (uint32_t)n);
+#else
+    const uint32_t hi = (uint32_t)((uint64_t)m * (uint32_t)n >> 32);
+#endif
+    return (int)((hi + (uint32_t)n) >> s);
   }
 };
 

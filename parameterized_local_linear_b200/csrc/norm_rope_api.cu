@@ -331,3 +331,5 @@ extern "C" int parallax_testing_norm_rope_stall_next(int timeout_ms) {
   stalled_timeout_ns = (unsigned long long)timeout_ms * 1000000ull;
   return PARALLAX_OK;
 }
+
+extern "C" int parallax_testing_divide(int n, int d) { return NrDivisor::of(d).quotient(n); }

@@ -21,12 +21,12 @@ constexpr int kRangeAlign = 64;  // partition ranges are multiples of one K/V ti
 
 // x / d for x >= 0, d > 0: one 32-bit division when x fits (the usual case;
 // a 64-bit division is a long software sequence on the critical path).
-__device__ __forceinline__ long long div_pos(long long x, long long d) {
+__host__ __device__ __forceinline__ long long div_pos(long long x, long long d) {
   if (x <= 0x7fffffffLL && d <= 0x7fffffffLL) return (long long)((unsigned)x / (unsigned)d);
   return x / d;
 }
 
-__device__ __forceinline__ int clamp_len(int n, int Lmax) {
+__host__ __device__ __forceinline__ int clamp_len(int n, int Lmax) {
   return n < 0 ? 0 : (n > Lmax ? Lmax : n);
 }
 
