@@ -38,8 +38,11 @@
 //    infinities) stays bf16, and its keys' weights are rounded to 17 bits and
 //    enter, times 2^8 too, as exact bf16 hi + lo pairs. A UMMA takes 16 keys, so
 //    each takes the form of its block. (Looking only at a block's largest value
-//    costs 4 drafted tokens 119 us instead of 131 and 512 rows 79 instead of 82,
-//    but loses the bits of a dimension that is small in every key.)
+//    takes 119 us instead of 120.5 for 4 drafted tokens, 79 instead of 83.5 for 512
+//    rows, 178 instead of 183 for a mixed batch, but loses the bits of a dimension
+//    that is small in every key. Of the ways to look at both: one vote over a warp's
+//    two blocks; a vote for each costs the drafts 129 us, blocks one after the other
+//    144, the exponent's bits moved instead of converted 122.)
 //
 // What bounds it. A 128 x 64 tile of D = 128 is 8.4 MFLOP of useful work and, at
 // the rates measured for these UMMAs one by one (S, T: 50 cycles per 16 dims, fed
@@ -388,18 +391,20 @@ __global__ void __launch_bounds__(kChThreads, 1)
   } else if (warp >= 10) {
     // ------------------------------- V: bf16 to fp16, rows past the end to 0 --
     constexpr int kWords = Geo::kH * 16 * 8 / 32;  // 16-byte words per lane
-    // bf16 bits of 2^8, of 2^-25 and of 2^-22 (from there fp16 is normal); what
-    // multiplies a pair of values below 2^8 by 2^8 (a 0 becomes 2^-119, 0 in fp16)
+    // bf16 bits of 2^8 and 2^-25, and what multiplies a pair of values below 2^8 by 2^8
+    // (a 0 becomes 2^-119, which is 0 in fp16)
     constexpr uint32_t kBelow = (127 + 16 - kChValueShift) << 7,
-                       kFrom = (127 - 17 - kChValueShift) << 7,
-                       kNormal = (127 - 14 - kChValueShift) << 7, kPair = 0x00010001u,
-                       kTimes = kPair * (kChValueShift << 7),
-                       kMove = kPair * (((15 - 127 + kChValueShift) & 31) << 10);
-    // Per half: max(far, 2 (|v| - kNormal)) of unsigned 16 bits, so that values below
-    // kNormal wrap to far ones. (v + v drops the signs; the low half's goes into the
-    // last bit of the high half, where it changes no comparison with an even bound.)
+                       kFrom = (127 - 17 - kChValueShift) << 7, kPair = 0x00010001u,
+                       kTimes = kPair * (kChValueShift << 7);
+    const auto turn = [](uint32_t v) {
+      v += kTimes;
+      return pack_f16x2(bf16_lo_to_float(v), bf16_hi_to_float(v));
+    };
+    // Per half: max(far, 2 (|v| - kFrom)) of unsigned 16 bits, so that values below kFrom
+    // wrap to far ones. (v + v drops the signs; the low half's goes into the last bit of
+    // the high half, where it changes no comparison with an even bound.)
     const auto range_max = [](uint32_t far, uint32_t v) {
-      return __viaddmax_u16x2(v + v, kPair * (0x10000u - 2 * kNormal), far);
+      return __viaddmax_u16x2(v + v, kPair * (0x10000u - 2 * kFrom), far);
     };
     bool ok = true;
     int jt = 0;
@@ -433,10 +438,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
               if ((warp - 10 + kChConvertWarps * y) * 16 + (i % 4) * 4 + lane / 8 >= left)
                 x[y][i] = make_uint4(0, 0, 0, 0);
         }
-        bool f16[kBlocks], direct[kBlocks];
+        uint32_t far[4] = {0, 0, 0, 0};  // independent chains
 #pragma unroll
-        for (int y = 0; y < kBlocks; ++y) {
-          uint32_t far[4] = {0, 0, 0, 0};  // independent chains
+        for (int y = 0; y < kBlocks; ++y)
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
             far[0] = range_max(far[0], x[y][i].x);
@@ -444,27 +448,26 @@ __global__ void __launch_bounds__(kChThreads, 1)
             far[2] = range_max(far[2], x[y][i].z);
             far[3] = range_max(far[3], x[y][i].w);
           }
-          const uint32_t f = __vmaxu2(__vmaxu2(far[0], far[1]), __vmaxu2(far[2], far[3]));
-          constexpr uint32_t kMost = kPair * (2 * (kBelow - kNormal) - 1);
-          direct[y] = __all_sync(0xffffffffu, __vmaxu2(f, kMost) == kMost);
-        }
+        constexpr uint32_t kMost = kPair * (2 * (kBelow - kFrom) - 1);
+        const uint32_t f = __vmaxu2(__vmaxu2(far[0], far[1]), __vmaxu2(far[2], far[3]));
+        bool f16[kBlocks];
+        if (__all_sync(0xffffffffu, __vmaxu2(f, kMost) == kMost)) {
 #pragma unroll
-        for (int y = 0; y < kBlocks; ++y) {
-          if (direct[y]) {  // all normal numbers of fp16: the exponent's low bits, moved
+          for (int y = 0; y < kBlocks; ++y) {
             f16[y] = true;
-            const auto turn = [&](uint32_t v) {
-              return (((v & 0x0fff0fffu) * 8 + kMove) & 0x7fff7fffu) | (v & 0x80008000u);
-            };
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
               uint4& v = x[y][i];
               v = make_uint4(turn(v.x), turn(v.y), turn(v.z), turn(v.w));
             }
-          } else {  // some are zeros or fp16's subnormal numbers, or out of its range
-            uint32_t far = 0;
+          }
+        } else {  // some are zeros or out of fp16's range: block by block
+#pragma unroll
+          for (int y = 0; y < kBlocks; ++y) {
+            uint32_t most = 0;
             const auto take = [&](uint32_t w) {  // (a 0 counts as the smallest in range)
               const uint32_t m = w & 0x7fff7fffu;
-              far = __vmaxu2(far, __vsub2(m, kPair * kFrom) & ~__vcmpeq2(m, 0));
+              most = __vmaxu2(most, __vsub2(m, kPair * kFrom) & ~__vcmpeq2(m, 0));
             };
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
@@ -473,12 +476,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
               take(x[y][i].z);
               take(x[y][i].w);
             }
-            f16[y] = __all_sync(0xffffffffu, max(far & 0xffffu, far >> 16) < kBelow - kFrom);
+            f16[y] = __all_sync(0xffffffffu, max(most & 0xffffu, most >> 16) < kBelow - kFrom);
             if (f16[y]) {
-              const auto turn = [&](uint32_t v) {
-                v += kTimes;
-                return pack_f16x2(bf16_lo_to_float(v), bf16_hi_to_float(v));
-              };
 #pragma unroll
               for (int i = 0; i < kWords; ++i) {
                 uint4& v = x[y][i];
@@ -486,6 +485,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
               }
             }
           }
+        }
+#pragma unroll
+        for (int y = 0; y < kBlocks; ++y) {
 #pragma unroll
           for (int i = 0; i < kWords; ++i) word(y, i) = x[y][i];
           if (lane == 0)
