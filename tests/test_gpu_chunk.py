@@ -554,3 +554,24 @@ def test_one_token_form_of_large_groups(D, G, probe):
         b = call(cu, causal=False)
         assert pl.parallax_workspace_status(ws) == (0, 0)
         assert torch.equal(a, b) and torch.equal(a, call(None, causal=False))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("probe", [True, False])
+def test_padding_and_broken_rows_stay_among_themselves(probe, bad):
+    """Rows of q and r past, before and between the sequences' tokens that are not finite
+    (padding that nobody wrote) change no other row, nor does one broken row of a
+    sequence, whose own outputs are not finite."""
+    seqs = [(5, 200), (70, 300), (1, 64)]
+    q, r, kp, vp, table, cu, lens = make(seqs, 64, 6, 2, 128, 125, pad=30)
+    q, r = q.roll(10, 0), r.roll(10, 0)
+    cu = cu + 10
+    o, S = reference(q, r if probe else None, kp, vp, table, cu, lens, True, 128 ** -0.5)
+    q[:10], r[:10], q[86:], r[86:] = bad, bad, bad, bad
+    q[40, 3], r[41, 2] = bad, bad
+    got = pl.parallax_prefill_paged(q, r if probe else None, kp, vp, table, lens, cu, probe=probe)
+    assert not got[:10].any() and not got[86:].any()
+    broken = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    broken[40, 3], broken[41, 2] = True, probe
+    assert not got[broken].isfinite().all(-1).any()
+    check(torch.where(broken[..., None], o.bfloat16(), got), o, S, 300)
