@@ -357,7 +357,8 @@ int parallax_varlen_prefill(const void* q, const void* r, const void* k, const v
  *     y_a = n_a cos_p - n_b sin_p,  y_b = n_a sin_p + n_b cos_p
  * for pair p of dimensions (a, b) = (p, p + rotary_dim / 2), or (2p, 2p + 1)
  * with interleaved != 0; dimensions from rotary_dim on are not rotated. All
- * arithmetic is fp32, rounded once to dtype. The pages' models are Qwen-3
+ * arithmetic is fp32, rounded once to dtype (so a row whose mean(x^2) passes
+ * fp32's range, |x| of 10^18 and more, is normed to 0). The pages' models are Qwen-3
  * ones ("Integrazioni AI personalizzate dopo l'attenzione Parallax"), whose
  * layers norm and rotate the heads this way; the probe is query-like (same
  * page, W_R acting on the layer input), so it may be normed and rotated too.

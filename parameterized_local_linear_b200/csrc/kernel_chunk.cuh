@@ -52,9 +52,11 @@
 // 2600 cycles, two warps per scheduler) and the V conversion (two warps) are each
 // near that. More softmax or converting warps leave too few registers (alternate
 // tiles to two sets of eight warps: 15% slower). Measured, 16 query on 8 kv heads
-// of 128: 2048 rows over 32768 keys 1050 us (1.0 PFLOP/s) at full clock, 1200
-// when the power limit holds the clock at 1.5 GHz; 512 rows over 8192 keys 79 us;
-// 4 drafted tokens of 32 sequences of 4096 keys 121 us (4.4 TB/s).
+// of 128, in a graph at full clock, and in a loop of calls, where the power limit
+// holds the clock at 1.5 to 1.8 GHz: 2048 rows over 32768 keys 1080 and 1265 us
+// (0.99 and 0.84 PFLOP/s), 512 rows over 8192 keys 83 and 91 us, 4 drafted tokens
+// of 32 sequences of 4096 keys 121 (4.4 TB/s) and 144 to 154 us. Softmax form: 900,
+// 65 and 115 us in a loop. D = 64: 865 and 71 us.
 //
 // Slots past a sequence's length may hold anything (NaN too): their scores are
 // masked before use, and the converting warps zero their V rows, which weight 0
