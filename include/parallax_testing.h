@@ -57,7 +57,7 @@ int parallax_testing_prefill_paged_stalled(
 
 /*
  * Changes the next call that this host thread makes of parallax_qk_norm_rope, its
- * backward pass or parallax_norm_rope_append (and that passes its argument checks):
+ * backward pass or parallax_norm_rope_append (one that is refused may use it up):
  * every wait is bounded by timeout_ms (1 .. 10000), and the first rows of each kind of
  * head are never loaded, so that the wait of the warp that has them runs out. It records
  * PARALLAX_DEVICE_STATUS_TIMEOUT, waits (bounded) for its own copies in flight and leaves

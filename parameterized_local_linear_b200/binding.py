@@ -595,7 +595,7 @@ def parallax_qk_norm_rope(q, r, k, cos_sin, positions=None, q_weight=None, r_wei
     """Per-head RMS norm and rotation of the query, probe and key heads.
 
     q [tokens, Hq, D], r like q or None, k [tokens, Hkv, D] (bf16 or fp32; token
-    rows may be slices of a wider buffer), weights [D] or None (no norm),
+    rows may be slices of a wider buffer), weights [D] of q's dtype or None (no norm),
     cos_sin as parallax_rope_table gives it, positions int32 [tokens] or None
     (0, 1, ... in each row of seq_len tokens). Returns (q, r, k), contiguous
     [tokens, H, D], or with seq_len = L [tokens / L, H, L, D]; out: three
